@@ -444,11 +444,110 @@ int yr_attn_decode_noalloc(const void *q_new, const void *k_new, const void *v_n
                            const yr_rope_table *tab, int window, int n_sink, void *stream);
 
 /*
+ * kv4 -- a KV cache held in 4 bits, and the calls that write, read and attend over it.
+ * Decode is memory-bound on the cache ("Long Context" concept page); this form moves and
+ * keeps 5d/4 bytes per token and KV head (160 at d = 128) where the bf16 caches take 4d
+ * (512).  One buffer holds keys and values:
+ *   kv4  bytes [B, Hkv, T_max, 5d/4], contiguous, 16-byte aligned; slot n of a sequence
+ *        belongs to position n.  Zeroed or uninitialised memory will do to begin with:
+ *        no call uses a slot that was not written, but yr_kv4_read of it.
+ * Row of a token and KV head:
+ *   [key codes d/2][value codes d/2][key (s, z) x d/32][value (s, z) x d/32]
+ *   Each 32 consecutive elements of the rotated key, and of the value, share an fp16 scale
+ *   s and minimum z; an element is a code n in 0 .. 15 that stands for s n + z:
+ *     z = fp16(min), s = fp16(max(0, (max - z) / 15)), n = clamp(rint((x - z) / s), 0, 15)
+ *   (n = 0 where s = 0), fp32 arithmetic, ties to even.  The key is rotated in fp64 and
+ *   rounded once to fp32 before that.  An element moves by at most s / 2 plus the fp16
+ *   roundings of z and s (15 / 2048 of a step and 2^-11 |z|).
+ *   Codes lie in the order in which the attention reads them, from the low nibble up, with
+ *   G = d / 32: 8 key codes at word r G + g (r = 0 .. 3) for elements 32g + 8r .. + 7, and 4
+ *   value codes at 16-bit unit c G + g (c = 0 .. 7) for elements 32g + 4c .. + 3.
+ * Range: |rotated k| and |v| must stay below 65520.  A value outside (or a NaN) is stored
+ *   as the nearest finite fp16 value (a NaN as 65504) and sets a range bit of the device
+ *   status word, which yr_device_status() reports as YR_ERANGE.
+ *
+ * kv4_row_bytes -- 5d/4, or 0 if d is not 64 or 128.
+ *
+ * kv4_write -- rotate (positions as in yr_prefill_prepare_kv), quantise and write keys and
+ *   values.  Row t of sequence b goes to slot (and stands at position) pos0 + starts[b] + t.
+ *   k, v    bf16 [B, Hkv, T, d], strides as in yr_attn_prefill (NULL = contiguous)
+ *   starts  int32 [B] on the device (nullable: 0 for every sequence)
+ *   counts  int32 [B] on the device, 0 <= counts[b] <= T (nullable: T for every sequence):
+ *           only rows t < counts[b] are read and written -- a padded batch.
+ *   Without starts and counts pos0 + T <= T_max is checked on the host.  Otherwise the
+ *   kernel checks each sequence: one whose rows do not lie in 0 .. T_max - 1 is skipped as
+ *   a whole and recorded in the device status word.  Slots outside the rows keep their
+ *   bytes.
+ *
+ * kv4_read -- rows back as values: row t of sequence b from slot pos0 + starts[b] + t.
+ *   k, v    bf16 (out_type YR_KV4_BF16) or fp16 (YR_KV4_FP16) [B, Hkv, T, d], strides as
+ *           above; one of them may be NULL.  s n + z is formed in fp32 and rounded once;
+ *           fp16 keeps +-65504 where it would pass that.
+ *   starts, counts and skipped sequences as in kv4_write; the output rows that are not
+ *   read (t >= counts[b], or a skipped sequence's) are set to zero if zero_rest is not 0,
+ *   else they keep their contents.
+ *
+ * attn_decode_kv4 -- yr_attn_decode over this cache: rotates q_new and k_new at position
+ *   L_b = cache_len[b], writes the new row into slot L_b, and returns attention of the
+ *   query over the rows 0 .. L_b as the cache holds them, the new one included, with the
+ *   window/sink rule and ALiBi as in yr_attn_decode.  Sequences whose length is out of
+ *   range get NaN and the status bit.
+ *   q_new bf16 [B, Hq, d]; k_new, v_new bf16 [B, Hkv, d]; o bf16 [B, Hq, d], contiguous
+ *   lse fp32 [B, Hq] (nullable)
+ *   k_stored, v_stored bf16 [B, Hkv, d] (nullable): the new row's values as stored
+ *   workspace: >= yr_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, d) bytes, 256-byte
+ *     aligned, for the partial results.  Calls that overlap need one each.
+ *   Precision: the query enters as two fp16 parts (22 bits) scaled by a power of two, the
+ *   codes exactly, scales in fp32; probabilities times scales enter the value product as
+ *   fp16 relative to the largest; all sums fp32.
+ *
+ * attn_prefill_chunk_kv4 -- yr_attn_prefill_chunk over this cache: writes the chunk's rows
+ *   into slots P0 .. P0+Tq-1, reads the rows 0 .. P0+Tq-1 back as fp16 into the workspace,
+ *   and attends over them.  A chunk's own keys are attended as stored, so the result does
+ *   not depend on where a prompt is cut (up to rounding), and Tq = 1 is a decode step.
+ *   With a window only the rows that some query of the chunk sees are used.
+ *   q, o bf16 [B, Hq, Tq, d]; k_new, v_new bf16 [B, Hkv, Tq, d], contiguous; lse fp32
+ *   [B, Hq, Tq] (nullable); q must stay in the fp16 range as in yr_attn_prefill.
+ *   workspace: 256-byte aligned; yr_attn_prefill_chunk_kv4_workspace_bytes() gives room
+ *     for the fp16 rows and for the split-KV partials of a short chunk.  The former are
+ *     needed -- yr_attn_prefill_workspace_bytes(B, Hkv, P0 + Tq, d) rounded up to 256 --
+ *     less than the rest limits the split.
+ *
+ * Errors: YR_EINVAL for NULL or misaligned pointers, sizes or flags out of range (B, Hkv
+ *   <= 65535 for all but attn_decode_kv4; positions <= 2^30), Hq not a multiple of Hkv, a
+ *   window/sink combination yr_attn_prefill rejects, or a small workspace;
+ *   YR_EUNSUPPORTED for d not 64/128, in attn_decode_kv4 Hq/Hkv > 16, or a non-sm_100
+ *   device; YR_ECUDA.
+ */
+#define YR_KV4_BF16 0
+#define YR_KV4_FP16 1
+size_t yr_kv4_row_bytes(int d);
+int yr_kv4_write(const void *k, const void *v, void *kv4, int B, int Hkv, int T, int d, int T_max,
+                 const int64_t *k_strides, const int64_t *v_strides, int pos0,
+                 const int32_t *starts, const int32_t *counts, const yr_rope_table *tab,
+                 void *stream);
+int yr_kv4_read(const void *kv4, void *k, void *v, int out_type, int B, int Hkv, int T, int d,
+                int T_max, const int64_t *k_strides, const int64_t *v_strides, int pos0,
+                const int32_t *starts, const int32_t *counts, int zero_rest, void *stream);
+size_t yr_attn_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int d);
+int yr_attn_decode_kv4(const void *q_new, const void *k_new, const void *v_new, void *kv4,
+                       const int32_t *cache_len, void *o, float *lse, void *k_stored,
+                       void *v_stored, int B, int Hq, int Hkv, int d, int T_max,
+                       const yr_rope_table *tab, int window, int n_sink, void *workspace,
+                       size_t workspace_bytes, void *stream);
+size_t yr_attn_prefill_chunk_kv4_workspace_bytes(int B, int Hq, int Hkv, int Tq, int d, int P0);
+int yr_attn_prefill_chunk_kv4(const void *q, const void *k_new, const void *v_new, void *kv4,
+                              void *o, float *lse, int B, int Hq, int Hkv, int Tq, int d, int P0,
+                              int T_max, const yr_rope_table *tab, int window, int n_sink,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * device_status -- synchronise `stream`, then read and clear the device status
  * word of the current device.  Returns YR_OK, YR_ETIMEOUT (a kernel gave up on
  * a wait; yr_last_error names where), YR_ERANGE (a prefill, chunk or block call
- * met a rotated query or key, or a value, outside the fp16 range), YR_EINVAL (a
- * decode cache length was out of range), or YR_ECUDA.  When several bits are
+ * met a rotated query or key, or a value, outside the fp16 range, or one was written
+ * to a 4-bit cache), YR_EINVAL (a decode cache length or a 4-bit cache's row range
+ * was out of range), or YR_ECUDA.  When several bits are
  * set the first of those codes is returned and the message names them all.
  */
 int yr_device_status(void *stream);

@@ -19,6 +19,7 @@ ROPE, PI, NTK, YARN = 0, 1, 2, 3
 NTK_DYNAMIC, YARN_DIMRAMP, FACTORS, ALIBI = 4, 5, 6, 7
 PAIR_INTERLEAVED, PAIR_HALF = 0, 1
 PAIRS = {"interleaved": PAIR_INTERLEAVED, "half": PAIR_HALF}
+KV4_BF16, KV4_FP16 = 0, 1
 METHODS = {"rope": ROPE, "pi": PI, "ntk": NTK, "yarn": YARN, "ntk_dynamic": NTK_DYNAMIC,
            "yarn_dimramp": YARN_DIMRAMP, "factors": FACTORS, "alibi": ALIBI}
 SYMBOLS = ("yr_rope_freq_table", "yr_attn_prefill_workspace_bytes", "yr_attn_prefill",
@@ -28,7 +29,10 @@ SYMBOLS = ("yr_rope_freq_table", "yr_attn_prefill_workspace_bytes", "yr_attn_pre
            "yr_prefill_attend_block", "yr_attn_merge",
            "yr_attn_decode_workspace_bytes", "yr_attn_decode", "yr_attn_decode_noalloc",
            "yr_host_prefill_workspace_bytes", "yr_host_prefill_create", "yr_host_prefill_run",
-           "yr_host_prefill_destroy", "yr_device_status", "yr_last_error", "yr_version")
+           "yr_host_prefill_destroy", "yr_kv4_row_bytes", "yr_kv4_write", "yr_kv4_read",
+           "yr_attn_decode_kv4_workspace_bytes", "yr_attn_decode_kv4",
+           "yr_attn_prefill_chunk_kv4_workspace_bytes", "yr_attn_prefill_chunk_kv4",
+           "yr_device_status", "yr_last_error", "yr_version")
 
 
 class YarnAttnError(RuntimeError):
@@ -114,6 +118,23 @@ def load(path: str | None = None, make_default: bool = False) -> ctypes.CDLL:
     lib.yr_host_prefill_run.restype = ci
     lib.yr_host_prefill_destroy.argtypes = [vp]
     lib.yr_host_prefill_destroy.restype = ci
+    lib.yr_kv4_row_bytes.argtypes = [ci]
+    lib.yr_kv4_row_bytes.restype = cs
+    lib.yr_kv4_write.argtypes = ([vp] * 3 + [ci] * 5 + [i64p] * 2 + [ci] + [vp] * 2 +
+                                 [ctypes.POINTER(RopeTable), vp])
+    lib.yr_kv4_write.restype = ci
+    lib.yr_kv4_read.argtypes = [vp] * 3 + [ci] * 6 + [i64p] * 2 + [ci] + [vp] * 2 + [ci, vp]
+    lib.yr_kv4_read.restype = ci
+    lib.yr_attn_decode_kv4_workspace_bytes.argtypes = [ci] * 4
+    lib.yr_attn_decode_kv4_workspace_bytes.restype = cs
+    lib.yr_attn_decode_kv4.argtypes = ([vp] * 9 + [ci] * 5 +
+                                       [ctypes.POINTER(RopeTable), ci, ci, vp, cs, vp])
+    lib.yr_attn_decode_kv4.restype = ci
+    lib.yr_attn_prefill_chunk_kv4_workspace_bytes.argtypes = [ci] * 6
+    lib.yr_attn_prefill_chunk_kv4_workspace_bytes.restype = cs
+    lib.yr_attn_prefill_chunk_kv4.argtypes = ([vp] * 6 + [ci] * 7 +
+                                              [ctypes.POINTER(RopeTable), ci, ci, vp, cs, vp])
+    lib.yr_attn_prefill_chunk_kv4.restype = ci
     lib.yr_device_status.argtypes = [vp]
     lib.yr_device_status.restype = ci
     lib.yr_last_error.argtypes = []
@@ -432,6 +453,170 @@ def attn_decode_noalloc(q_new, k_new, v_new, k_cache, v_cache, cache_len, table:
         _ptr(out), _ptr(lse), _ptr(q_rot_dbg), B, Hq, Hkv, d, T_max, ctypes.byref(table),
         int(window), int(n_sink), _stream(stream))
     _check(rc)
+    return out
+
+
+def kv4_row_bytes(d: int) -> int:
+    return int(load().yr_kv4_row_bytes(d))
+
+
+def kv4_cache(B: int, Hkv: int, T_max: int, d: int, device="cuda") -> torch.Tensor:
+    """An empty 4-bit KV cache: zeroed uint8 [B, Hkv, T_max, 5d/4]."""
+    n = kv4_row_bytes(d)
+    if n == 0:
+        raise ValueError("kv4_cache: d must be 64 or 128")
+    return torch.zeros((B, Hkv, T_max, n), dtype=torch.uint8, device=device)
+
+
+def _kv4_tensors(fn, kv4, tensors):
+    """Checks a 4-bit cache and the tensors (name, tensor, dtype, shape) used with it: all
+    contiguous on its device, except those whose shape is given as a list, which may be
+    strided.  None is an argument left out."""
+    dev = kv4.device
+    if not kv4.is_cuda or kv4.dtype != torch.uint8 or kv4.dim() != 4 or not kv4.is_contiguous():
+        raise ValueError(f"{fn}: kv4 must be a contiguous uint8 CUDA tensor [B, Hkv, T_max, 5d/4]")
+    for name, t, dtype, shape in tensors:
+        if t is None:
+            continue
+        if t.device != dev or t.dtype != dtype:
+            raise ValueError(f"{fn}: {name} must be a {dtype} tensor on {dev}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{fn}: {name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+        if not isinstance(shape, list) and not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _kv4_call(dev, fn, args, stream):
+    """fn(*args, stream) with the tensors' device current, on its current stream if none is given."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def _kv4_strides(fn, name, t):
+    """Strides over b, h and t.  Those of axes of one element are never used and may be
+    anything in torch; they are passed on as those of a contiguous tensor."""
+    if t.stride(3) != 1:
+        raise ValueError(f"{fn}: {name} must have unit stride over d")
+    st, n = [], t.shape[3]
+    for i in (2, 1, 0):
+        st.insert(0, t.stride(i) if t.shape[i] > 1 else n)
+        n = max(n, st[0] * t.shape[i])
+    return (ctypes.c_int64 * 3)(*st)
+
+
+def kv4_write(k, v, kv4, table: RopeTable, pos0: int = 0, starts=None, counts=None, stream=None):
+    """Rotate, quantise and write k, v [B,Hkv,T,d] bf16 (any strides with unit stride over d)
+    into the 4-bit cache: row t of sequence b goes to slot pos0 + starts[b] + t.  starts and
+    counts are int32 [B] on the device (None: 0 and T); rows t >= counts[b] are left out.
+    Returns kv4."""
+    B, Hkv, T, d = k.shape
+    _kv4_tensors("kv4_write", kv4, [
+        ("kv4", kv4, torch.uint8, (B, Hkv, kv4.shape[2], 5 * d // 4)),
+        ("k", k, torch.bfloat16, [B, Hkv, T, d]), ("v", v, torch.bfloat16, [B, Hkv, T, d]),
+        ("starts", starts, torch.int32, (B,)), ("counts", counts, torch.int32, (B,))])
+    _kv4_call(kv4.device, load().yr_kv4_write,
+              (_ptr(k), _ptr(v), _ptr(kv4), B, Hkv, T, d, kv4.shape[2],
+               _kv4_strides("kv4_write", "k", k), _kv4_strides("kv4_write", "v", v), int(pos0),
+               _ptr(starts), _ptr(counts), ctypes.byref(table)), stream)
+    return kv4
+
+
+def kv4_read(kv4, T: int, pos0: int = 0, starts=None, counts=None, dtype=torch.bfloat16,
+             k=None, v=None, stream=None):
+    """Rows of the 4-bit cache as values: row t of sequence b from slot pos0 + starts[b] + t,
+    t < counts[b] (starts, counts as in kv4_write).  Returns (k, v) [B,Hkv,T,d] in `dtype`
+    (bf16 or fp16); outputs given as k and v are written in place (any strides with unit
+    stride over d) and keep the rows that are not read, others are allocated, with zeros
+    there."""
+    B, Hkv, T_max, n = kv4.shape
+    d = n * 4 // 5
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("kv4_read: dtype must be torch.bfloat16 or torch.float16")
+    zero_rest = k is None and v is None
+    if zero_rest:
+        k = torch.empty((B, Hkv, T, d), dtype=dtype, device=kv4.device)
+        v = torch.empty_like(k)
+    elif k is None:
+        k = torch.zeros((B, Hkv, T, d), dtype=dtype, device=kv4.device)
+    elif v is None:
+        v = torch.zeros((B, Hkv, T, d), dtype=dtype, device=kv4.device)
+    _kv4_tensors("kv4_read", kv4, [
+        ("kv4", kv4, torch.uint8, (B, Hkv, T_max, 5 * d // 4)),
+        ("k", k, dtype, [B, Hkv, T, d]), ("v", v, dtype, [B, Hkv, T, d]),
+        ("starts", starts, torch.int32, (B,)), ("counts", counts, torch.int32, (B,))])
+    _kv4_call(kv4.device, load().yr_kv4_read,
+              (_ptr(kv4), _ptr(k), _ptr(v), KV4_BF16 if dtype == torch.bfloat16 else KV4_FP16, B,
+               Hkv, T, d, T_max, _kv4_strides("kv4_read", "k", k),
+               _kv4_strides("kv4_read", "v", v), int(pos0), _ptr(starts), _ptr(counts),
+               int(zero_rest)), stream)
+    return k, v
+
+
+def attn_decode_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load().yr_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, d))
+
+
+def attn_decode_kv4(q_new, k_new, v_new, kv4, cache_len, table: RopeTable, window: int = 0,
+                    n_sink: int = 0, out=None, lse=None, k_stored=None, v_stored=None,
+                    workspace=None, stream=None):
+    """Single-token decode over the 4-bit cache.  q_new [B,Hq,d], k_new/v_new [B,Hkv,d] bf16,
+    cache_len int32 [B] on the device.  Writes slot cache_len[b]; returns the output [B,Hq,d]
+    bf16.  lse fp32 [B,Hq] and k_stored, v_stored bf16 [B,Hkv,d] (the new row as the cache
+    holds it) are filled if given."""
+    B, Hq, d = q_new.shape
+    Hkv, T_max = kv4.shape[1], kv4.shape[2]
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=kv4.device)
+    if workspace is None:
+        workspace = torch.empty(attn_decode_kv4_workspace_bytes(B, Hq, Hkv, d),
+                                dtype=torch.uint8, device=kv4.device)
+    bf = torch.bfloat16
+    _kv4_tensors("attn_decode_kv4", kv4, [
+        ("kv4", kv4, torch.uint8, (B, Hkv, T_max, 5 * d // 4)), ("q_new", q_new, bf, (B, Hq, d)),
+        ("k_new", k_new, bf, (B, Hkv, d)), ("v_new", v_new, bf, (B, Hkv, d)),
+        ("cache_len", cache_len, torch.int32, (B,)), ("out", out, bf, (B, Hq, d)),
+        ("lse", lse, torch.float32, (B, Hq)), ("k_stored", k_stored, bf, (B, Hkv, d)),
+        ("v_stored", v_stored, bf, (B, Hkv, d)),
+        ("workspace", workspace, workspace.dtype, tuple(workspace.shape))])
+    _kv4_call(kv4.device, load().yr_attn_decode_kv4,
+              (_ptr(q_new), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(cache_len), _ptr(out),
+               _ptr(lse), _ptr(k_stored), _ptr(v_stored), B, Hq, Hkv, d, T_max,
+               ctypes.byref(table), int(window), int(n_sink), _ptr(workspace),
+               workspace.numel() * workspace.element_size()), stream)
+    return out
+
+
+def attn_prefill_chunk_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, Tq: int, d: int,
+                                           P0: int) -> int:
+    return int(load().yr_attn_prefill_chunk_kv4_workspace_bytes(B, Hq, Hkv, Tq, d, P0))
+
+
+def attn_prefill_chunk_kv4(q, k_new, v_new, kv4, P0: int, table: RopeTable, window: int = 0,
+                           n_sink: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Chunked prefill over the 4-bit cache: q [B,Hq,Tq,d], k_new/v_new [B,Hkv,Tq,d] bf16 at
+    positions P0.. .  Writes slots P0..P0+Tq-1 and attends over slots 0..P0+Tq-1 as the cache
+    holds them; returns the output [B,Hq,Tq,d] bf16.  lse fp32 [B,Hq,Tq] is filled if given."""
+    B, Hq, Tq, d = q.shape
+    Hkv, T_max = kv4.shape[1], kv4.shape[2]
+    if out is None:
+        out = torch.empty((B, Hq, Tq, d), dtype=torch.bfloat16, device=kv4.device)
+    if workspace is None:
+        workspace = torch.empty(
+            attn_prefill_chunk_kv4_workspace_bytes(B, Hq, Hkv, Tq, d, int(P0)),
+            dtype=torch.uint8, device=kv4.device)
+    bf = torch.bfloat16
+    _kv4_tensors("attn_prefill_chunk_kv4", kv4, [
+        ("kv4", kv4, torch.uint8, (B, Hkv, T_max, 5 * d // 4)), ("q", q, bf, (B, Hq, Tq, d)),
+        ("k_new", k_new, bf, (B, Hkv, Tq, d)), ("v_new", v_new, bf, (B, Hkv, Tq, d)),
+        ("out", out, bf, (B, Hq, Tq, d)), ("lse", lse, torch.float32, (B, Hq, Tq)),
+        ("workspace", workspace, workspace.dtype, tuple(workspace.shape))])
+    _kv4_call(kv4.device, load().yr_attn_prefill_chunk_kv4,
+              (_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(out), _ptr(lse), B, Hq, Hkv, Tq,
+               d, int(P0), T_max, ctypes.byref(table), int(window), int(n_sink),
+               _ptr(workspace), workspace.numel() * workspace.element_size()), stream)
     return out
 
 

@@ -12,7 +12,9 @@
 #include <unordered_map>
 
 #include "../../include/yarnattn.h"
+#include "decode4_sm100.cuh"
 #include "decode_sm100.cuh"
+#include "kv4_sm100.cuh"
 #include "kvprep_sm100.cuh"
 #include "merge_sm100.cuh"
 #include "prefill_sm100.cuh"
@@ -583,6 +585,44 @@ int choose_split(int sm_count, int B, int Hq, int Hkv, int Tq, int P0, int windo
     return best;
 }
 
+// Causal attention of Tq query rows after P0 keys over the planes `kv`: in one piece, or
+// split over the keys where that fills the GPU and split_ws holds the partials.
+int attend_planes(const void *q, void *o, float *lse, int B, int Hq, int Hkv, int Tq, int d,
+                  int P0, const long long qs[3], const long long os[3], const yr_rope_table *tab,
+                  int window, int n_sink, const KvPlanes &kv, void *split_ws,
+                  size_t split_ws_bytes, int sm_count, cudaStream_t st) {
+    const int Tk = P0 + Tq;
+    const size_t share = split_share_bytes(B, Hq, Tq, d);
+    const int n_split = split_ws ? choose_split(sm_count, B, Hq, Hkv, Tq, P0, window, split_ws_bytes,
+                                                share)
+                                 : 1;
+    if (n_split == 1)
+        return launch_attend(q, o, lse, nullptr, B, Hq, Hkv, Tq, d, qs, os, tab, 1, window,
+                             n_sink, kv, st, Tk, P0);
+    // Split-KV: the shares' fp32 partials, then their log-sum-exp merge into o.
+    const long long rows = static_cast<long long>(B) * Hq * Tq;
+    float *o_part = static_cast<float *>(split_ws);
+    float *lse_part = o_part + n_split * rows * d;
+    int rc = launch_attend(q, nullptr, lse_part, nullptr, B, Hq, Hkv, Tq, d, qs, os, tab, 1, window,
+                           n_sink, kv, st, Tk, P0, 0, o_part, n_split);
+    if (rc != YR_OK) return rc;
+    yr::SplitMergeParams mp;
+    mp.o_part = o_part;
+    mp.lse_part = lse_part;
+    mp.o = static_cast<__nv_bfloat16 *>(o);
+    mp.lse = lse;
+    mp.rows = rows;
+    mp.d = d;
+    mp.n_split = n_split;
+    long long blocks = (rows * (d / 8) + 255) / 256;
+    const long long cap = static_cast<long long>(sm_count) * 16;
+    if (blocks > cap) blocks = cap;
+    yr::split_merge_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(mp);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail("split_merge_kernel launch", e);
+    return YR_OK;
+}
+
 int chunk_call(const char *fn, const void *q, const void *k_new, const void *v_new,
                void *k_cache, void *v_cache, void *o, float *lse, int B, int Hq, int Hkv,
                int Tq, int d, int P0, int T_max, const yr_rope_table *tab, int window,
@@ -634,36 +674,8 @@ int chunk_call(const char *fn, const void *q, const void *k_new, const void *v_n
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail("chunk_prep_kernel launch", e);
     }
-    const size_t share = split_share_bytes(B, Hq, Tq, d);
-    const int n_split = split_ws ? choose_split(sm_count, B, Hq, Hkv, Tq, P0, window, split_ws_bytes,
-                                                share)
-                                 : 1;
-    const KvPlanes kv{k16, v16, ld16};
-    if (n_split == 1)
-        return launch_attend(q, o, lse, nullptr, B, Hq, Hkv, Tq, d, qs, os, tab, 1, window,
-                             n_sink, kv, st, Tk, P0);
-    // Split-KV: the shares' fp32 partials, then their log-sum-exp merge into o.
-    const long long rows = static_cast<long long>(B) * Hq * Tq;
-    float *o_part = static_cast<float *>(split_ws);
-    float *lse_part = o_part + n_split * rows * d;
-    rc = launch_attend(q, nullptr, lse_part, nullptr, B, Hq, Hkv, Tq, d, qs, os, tab, 1, window,
-                       n_sink, kv, st, Tk, P0, 0, o_part, n_split);
-    if (rc != YR_OK) return rc;
-    yr::SplitMergeParams mp;
-    mp.o_part = o_part;
-    mp.lse_part = lse_part;
-    mp.o = static_cast<__nv_bfloat16 *>(o);
-    mp.lse = lse;
-    mp.rows = rows;
-    mp.d = d;
-    mp.n_split = n_split;
-    long long blocks = (rows * (d / 8) + 255) / 256;
-    const long long cap = static_cast<long long>(sm_count) * 16;
-    if (blocks > cap) blocks = cap;
-    yr::split_merge_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(mp);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail("split_merge_kernel launch", e);
-    return YR_OK;
+    return attend_planes(q, o, lse, B, Hq, Hkv, Tq, d, P0, qs, os, tab, window, n_sink,
+                         KvPlanes{k16, v16, ld16}, split_ws, split_ws_bytes, sm_count, st);
 }
 
 }  // namespace yr_host
@@ -970,7 +982,12 @@ extern "C" int yr_device_status(void *stream) {
     if (v & yr::kStatusRange)
         msg += " prefill-operand-outside-fp16-range (|rotated q|, |rotated k| or |v| >= 65520,"
                " or not a number)";
+    if (v & yr::kStatusKv4Range)
+        msg += " 4-bit-cache-operand-outside-fp16-range (|rotated k| or |v| >= 65520, or not a"
+               " number)";
     set_error(msg);
     if (v & 0xFFu) return YR_ETIMEOUT;
-    return (v & yr::kStatusRange) ? YR_ERANGE : YR_EINVAL;
+    return (v & (yr::kStatusRange | yr::kStatusKv4Range)) ? YR_ERANGE : YR_EINVAL;
 }
+
+#include "kv4_entry.cuh"

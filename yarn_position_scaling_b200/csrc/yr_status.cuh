@@ -9,9 +9,10 @@ enum StatusBits : unsigned {
     kStatusTimeoutMma = 1u << 1,      // prefill MMA issuer gave up waiting
     kStatusTimeoutSoftmax = 1u << 2,  // prefill softmax warps gave up waiting
     kStatusTimeoutDrain = 1u << 3,    // prefill teardown gave up draining copies/MMAs
-    kStatusBadCacheLen = 1u << 8,     // decode: a cache length outside [0, T_max-1]
+    kStatusBadCacheLen = 1u << 8,     // a cache length or row range outside the cache
     kStatusRange = 1u << 9,           // prefill: an operand outside the fp16 range (|x| >= 65520,
                                       // or not a number) after rotation or conversion
+    kStatusKv4Range = 1u << 10,       // 4-bit cache: a key or value to write outside that range
 };
 // Largest magnitude that rounds to a finite fp16 (65504 is the largest finite value;
 // round-to-nearest sends [65504, 65520) to it and anything from 65520 on to infinity).
