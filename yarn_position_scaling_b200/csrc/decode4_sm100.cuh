@@ -14,10 +14,12 @@
 
 namespace yr {
 
-constexpr int kDec4Chunk = 128;      // least keys per block
+constexpr int kDec4Chunk = 128;      // least keys per block: a tile for each warp
 constexpr int kDec4MaxBlocks = 640;  // most blocks of the split launch
-constexpr int kDec4Threads = 128;
-constexpr int kDec4Tile = 32;
+constexpr int kDec4Warps = 4;
+constexpr int kDec4Threads = kDec4Warps * 32;
+constexpr int kDec4Tile = 32;  // keys of one bulk copy
+constexpr int kDec4Stages = 3;
 
 struct Decode4Params {
     const __nv_bfloat16 *q_new;          // [B][Hq][d]
@@ -34,6 +36,7 @@ struct Decode4Params {
     int window, n_sink;
     float sl2;  // softmax scale times log2 e
     int alibi;
+    uint64_t timeout_ns;
     double turns[64];
 };
 
@@ -108,14 +111,92 @@ __device__ __forceinline__ void dec4_append(const Decode4Params &p, int b, int k
     }
 }
 
-template <int HD, bool kHalf>
-__global__ void __launch_bounds__(kDec4Threads)
+// ---------------------------------------------------------------------------- fragments
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                          uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], "
+        "%2, [%3], %4;" ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ float lo_f(uint32_t sz) {
+    return __low2float(*reinterpret_cast<const __half2 *>(&sz));
+}
+__device__ __forceinline__ float hi_f(uint32_t sz) {
+    return __high2float(*reinterpret_cast<const __half2 *>(&sz));
+}
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// The exponent e with x in [2^e, 2^(e+1)), for normal x > 0.
+__device__ __forceinline__ int exponent_of(float x) { return (__float_as_int(x) >> 23) - 127; }
+
+// Key of a tile's fragment row i (0 .. 15).  Neighbouring lanes' shared-memory reads then
+// fall into different banks: rows are 160 (80) bytes apart, a fragment reads 16 (8) bytes by
+// four lanes of a row for the keys and 8 (4) bytes by eight lanes for the values.
+template <int HD>
+__device__ __forceinline__ int dec4_key(int i) {
+    const int h = (i >> 2) & 1, m = (i >> 1) & 1, b = i & 1;
+    if constexpr (HD == 128)
+        return (i & 8) + 4 * h + m + 2 * (b ^ h);
+    else
+        return (i & 8) + 2 * (i & 3) + h;
+}
+
+template <int HD, int NT>
+struct Decode4Smem {
+    static constexpr int kStageBytes = kDec4Tile * kv4_row_bytes(HD);
+    alignas(128) uint8_t ring[kDec4Warps][kDec4Stages][kStageBytes];  // also the warps' outputs
+    alignas(16) uint8_t new_row[kv4_row_bytes(HD)];
+    double2 cs[HD / 2];
+    float q[8 * NT][HD];
+    float q_scale[8 * NT];  // the power of two that the head's query was multiplied by
+    float m[kDec4Warps][8 * NT], l[kDec4Warps][8 * NT];
+    uint64_t full[kDec4Warps][kDec4Stages];
+    int abort;
+};
+template <int HD, int NT>
+constexpr size_t decode4_smem_bytes() {
+    return sizeof(Decode4Smem<HD, NT>) + 128;
+}
+
+// Each warp takes every fourth 32-key tile of the block's share by itself: a ring of bulk
+// copies with a barrier per stage, no block-wide wait in the loop, and a partial result
+// (max, sum, outputs) of its own, joined at the share's end.
+//   Scores: S^T[16 keys x 8 heads] by m16n8k16, keys as A.  A code enters as the fp16
+//   number with its four bits as the lowest of the mantissa, n 2^-24 (or n 2^-20 from the
+//   byte's upper half, where the query is scaled by 2^-4): a mask is the whole conversion,
+//   and exact.  The query is split into two fp16 parts.  Each 32-element group has its own
+//   accumulator, multiplied by the row's s in fp32; z (sum of q over the group) is one more
+//   product of fp16 operands, again with the sum in two parts.
+//   Outputs: O^T[16 dims x 8 heads], value codes as A in the same way, B = p s F with a
+//   power of two F per group that keeps it between fp16's ends; sum p z in fp32.
+//   The running maximum is raised only when a score passes it by 2^8, and F is changed only
+//   then or when a product nears overflow, so the common tile costs one vote.
+template <int HD, int NT, bool kHalf>
+__global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
     decode4_split_kernel(const __grid_constant__ Decode4Params p) {
+    using Smem = Decode4Smem<HD, NT>;
     constexpr int kRow = kv4_row_bytes(HD), G = HD / kKv4Group;
-    __shared__ float q[16][HD], k[kDec4Tile][HD + 1], v[kDec4Tile][HD], sc[16][kDec4Tile];
-    __shared__ float m_run[16], l_run[16], al[16];
-    __shared__ double2 cs[HD / 2];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = p.group;
+    extern __shared__ uint8_t smem_raw[];
+    Smem *sm = reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
+                                        ~static_cast<uintptr_t>(127));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane >> 2, r = lane & 3;
+    const int g = p.group;
     const long long total = dec4_total(p, lane);
     const long long U = dec4_units_per_block(p, total);
     const long long u_lo = static_cast<long long>(blockIdx.x) * U;
@@ -123,116 +204,434 @@ __global__ void __launch_bounds__(kDec4Threads)
     if (blockIdx.x == 0 && tid == 0)
         for (int b = 0; b < p.B; ++b)
             if (p.cache_len[b] < 0 || p.cache_len[b] > p.T_max - 1) raise_status(kStatusBadCacheLen);
+    if (u_lo >= u_hi) return;
+    if (tid == 0) {
+        for (int w = 0; w < kDec4Warps; ++w)
+            for (int s = 0; s < kDec4Stages; ++s) mbar_init(&sm->full[w][s], 1);
+        sm->abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    uint32_t n_loads = 0, n_waits = 0;  // of this warp's ring, over all segments
+    const uint64_t policy = l2_policy_evict_first();
+    bool ok = true;
+
+    // Sequences before the first one of this block.
+    int b = 0;
     long long seg0 = 0;
-    for (int b = 0; b < p.B && seg0 < u_hi; ++b) {
+    for (long long v; b < p.B && seg0 + (v = dec4_seq_units(p, b)) <= u_lo; ++b) seg0 += v;
+    for (; b < p.B && seg0 < u_hi; ++b) {
         const int L = p.cache_len[b];
         const DecRanges rg = dec4_ranges(p, L);
-        const int V = rg.len1 + rg.len2;
+        const long long V = rg.len1 + rg.len2;
         if (V == 0) continue;
-        for (int kvh = 0; kvh < p.Hkv && seg0 < u_hi; ++kvh, seg0 += V) {
-            if (seg0 + V <= u_lo) continue;
-            const int a = static_cast<int>(max(u_lo, seg0) - seg0);
-            const int e = static_cast<int>(min(u_hi, seg0 + V) - seg0);
+        int kvh = seg0 < u_lo ? static_cast<int>((u_lo - seg0) / V) : 0;
+        seg0 += kvh * V;
+        for (; kvh < p.Hkv && seg0 < u_hi; ++kvh, seg0 += V) {
+            // Units [u0, u1) of the segment are this block's: keys of the first range, then
+            // of the second.
+            const int u0 = static_cast<int>(max(u_lo, seg0) - seg0);
+            const int u1 = static_cast<int>(min(u_hi, seg0 + V) - seg0);
+            const int lo1 = min(u0, rg.len1), hi1 = min(u1, rg.len1);
+            const int lo2 = rg.lo2 + max(u0, rg.len1) - rg.len1;
+            const int hi2 = rg.lo2 + max(u1, rg.len1) - rg.len1;
+            const int n_t1 = (hi1 - lo1 + kDec4Tile - 1) / kDec4Tile;
+            const int n_tiles = n_t1 + (hi2 - lo2 + kDec4Tile - 1) / kDec4Tile;
+            const bool has_L = u1 == V;  // the new row is the last of this block's keys
             uint8_t *plane = p.kv4 + (static_cast<long long>(b) * p.Hkv + kvh) * p.T_max * kRow;
+            auto tile_lo = [&](int i) { return i < n_t1 ? lo1 + i * kDec4Tile : lo2 + (i - n_t1) * kDec4Tile; };
+            auto tile_n = [&](int i) { return min(kDec4Tile, (i < n_t1 ? hi1 : hi2) - tile_lo(i)); };
+            auto load = [&](int i) {  // the cached rows of tile i: all but the new one
+                const int s = n_loads % kDec4Stages;
+                const int n = tile_n(i) - (has_L && i == n_tiles - 1 ? 1 : 0);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm->full[warp][s], n * kRow);
+                    if (n > 0)
+                        bulk_load(smem_u32(sm->ring[warp][s]), plane + static_cast<long long>(tile_lo(i)) * kRow,
+                                  n * kRow, &sm->full[warp][s], policy);
+                }
+                ++n_loads;
+            };
+#pragma unroll
+            for (int s = 0; s < kDec4Stages; ++s)
+                if (warp + s * kDec4Warps < n_tiles) load(warp + s * kDec4Warps);
+
+            // ---- queries: rotated, scaled, as fragments of two fp16 parts
+            for (int i = tid; i < HD / 2; i += kDec4Threads) sm->cs[i] = kv4_cos_sin(L, p.turns[i]);
             __syncthreads();
-            for (int i = tid; i < HD / 2; i += kDec4Threads) cs[i] = kv4_cos_sin(L, p.turns[i]);
-            if (tid < 16) {
-                m_run[tid] = -INFINITY;
-                l_run[tid] = 0.f;
+            for (int i = tid; i < 8 * NT * (HD / 8); i += kDec4Threads) {
+                const int h = i / (HD / 8), ch = i % (HD / 8);
+                float y[8], mx = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = 0.f;
+                if (h < g)
+                    kv4_rotate8<HD, kHalf>(p.q_new + (static_cast<long long>(b) * p.Hq + kvh * g + h) * HD,
+                                           ch, sm->cs, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(y[e]));
+#pragma unroll
+                for (int off = 1; off < HD / 8; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                // Largest element to [2^7, 2^8): both parts and their group sums fit fp16,
+                // and the second part keeps its bits.
+                const int e2 = mx > 0.f ? max(-100, min(127, exponent_of(mx))) : 0;
+                const float f = pow2i(7 - e2);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sm->q[h][8 * ch + e] = y[e] * f;
+                if (ch == 0) sm->q_scale[h] = pow2i(e2 - 7);
+            }
+            const int last_warp = (n_tiles - 1) % kDec4Warps;
+            if (has_L && warp == last_warp) {
+                dec4_append<HD, kHalf>(p, b, kvh, sm->new_row, sm->cs, lane);
+                __syncwarp();
+                if (lane < kRow / 16)
+                    reinterpret_cast<uint4 *>(plane + static_cast<long long>(L) * kRow)[lane] =
+                        reinterpret_cast<const uint4 *>(sm->new_row)[lane];
             }
             __syncthreads();
-            if (e == V && warp == 0) dec4_append<HD, kHalf>(p, b, kvh, plane + static_cast<long long>(L) * kRow, cs, lane);
-            for (int i = tid; i < g * (HD / 8); i += kDec4Threads) {
-                const int h = i / (HD / 8), c = i % (HD / 8);
-                float y[8];
-                kv4_rotate8<HD, kHalf>(p.q_new + (static_cast<long long>(b) * p.Hq + kvh * g + h) * HD, c, cs, y);
+            uint32_t qh[2 * G][NT][2], ql[2 * G][NT][2], qz[NT];
+            float x_scale[NT][2], slope2[NT][2];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) q[h][8 * c + x] = y[x];
+            for (int nt = 0; nt < NT; ++nt) {
+                const float *q = sm->q[nt * 8 + c];
+                float zs[2] = {0.f, 0.f};  // group sums of this lane's part of the z product
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int at = 32 * gr + 8 * r + 2 * part + k;
+                            const float f = k == 0 ? 1.f : 0.0625f;
+                            const float v0 = q[at] * f, v1 = q[at + 4] * f;
+                            const __half h0 = __float2half_rn(v0), h1 = __float2half_rn(v1);
+                            const __half2 hv = __halves2half2(h0, h1);
+                            qh[2 * gr + part][nt][k] = *reinterpret_cast<const uint32_t *>(&hv);
+                            ql[2 * gr + part][nt][k] = pack_half2(v0 - __half2float(h0), v1 - __half2float(h1));
+                        }
+                    if (gr / 2 == (r & 1)) {
+                        float s = 0.f;
+                        for (int j = 0; j < 32; ++j) s += q[32 * gr + j];
+                        zs[gr & 1] = s;
+                    }
+                }
+                const __half h0 = __float2half_rn(zs[0]), h1 = __float2half_rn(zs[1]);
+                const __half2 hv = __halves2half2(h0, h1);
+                qz[nt] = r < 2 ? *reinterpret_cast<const uint32_t *>(&hv)
+                               : pack_half2(zs[0] - __half2float(h0), zs[1] - __half2float(h1));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int col = nt * 8 + 2 * r + j;
+                    x_scale[nt][j] = p.sl2 * sm->q_scale[col];
+                    slope2[nt][j] = p.alibi ? exp2f(-8.0f * static_cast<float>(kvh * g + col + 1) /
+                                                    static_cast<float>(p.Hq)) * 1.4426950408889634f
+                                            : 0.f;
+                }
             }
-            float acc[16];
+
+            float o[G][2][NT][4], w[NT][2][G], l[NT][2], M[NT][2], F[G];
+            uint32_t top[G];  // largest B operand of each group so far, per head parity
 #pragma unroll
-            for (int h = 0; h < 16; ++h) acc[h] = 0.f;
-            const int dim = tid % HD;
-            for (int u = a; u < e; u += kDec4Tile) {
-                __syncthreads();
-                const int cnt = min(kDec4Tile, e - u);
-                for (int i = tid; i < kDec4Tile * (HD / 8); i += kDec4Threads) {
-                    const int r = i / (HD / 8), c = i % (HD / 8);
-                    float x[8], y[8];
+            for (int gr = 0; gr < G; ++gr) {
+                F[gr] = 1.f;
+                top[gr] = 0;
+            }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.f;
-                    if (r < cnt) {
-                        const int n = u + r < rg.len1 ? u + r : rg.lo2 + u + r - rg.len1;
-                        const uint8_t *row = plane + static_cast<long long>(n) * kRow;
-                        const __half2 *par = reinterpret_cast<const __half2 *>(row + HD);
-                        const uint16_t *vu = reinterpret_cast<const uint16_t *>(row + HD / 2);
-                        const int cg = c >> 2, cr = c & 3;
-                        kv4_values8(reinterpret_cast<const uint32_t *>(row)[cr * G + cg], par[cg], x);
-                        kv4_values8(vu[2 * cr * G + cg] | (static_cast<uint32_t>(vu[(2 * cr + 1) * G + cg]) << 16),
-                                    par[G + cg], y);
-                    }
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        k[r][8 * c + j] = x[j];
-                        v[r][8 * c + j] = y[j];
+                for (int j = 0; j < 2; ++j) {
+                    M[nt][j] = -INFINITY;
+                    l[nt][j] = 0.f;
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        w[nt][j][gr] = 0.f;
+                        o[gr][0][nt][j] = o[gr][0][nt][j + 2] = 0.f;
+                        o[gr][1][nt][j] = o[gr][1][nt][j + 2] = 0.f;
                     }
                 }
-                __syncthreads();
-                for (int i = tid; i < g * kDec4Tile; i += kDec4Threads) {
-                    const int h = i / kDec4Tile, r = i % kDec4Tile;
-                    float x = -INFINITY;
-                    if (r < cnt) {
-                        const int n = u + r < rg.len1 ? u + r : rg.lo2 + u + r - rg.len1;
-                        float dot = 0.f;
-                        for (int j = 0; j < HD; ++j) dot = fmaf(q[h][j], k[r][j], dot);
-                        x = dot * p.sl2;
-                        if (p.alibi)
-                            x -= exp2f(-8.f * static_cast<float>(kvh * g + h + 1) / static_cast<float>(p.Hq)) *
-                                 1.4426950408889634f * static_cast<float>(L - n);
-                    }
-                    sc[h][r] = x;
+
+            for (int i = warp; i < n_tiles; i += kDec4Warps) {
+                const int s = n_waits % kDec4Stages;
+                ok = ok && mbar_wait_drain(&sm->full[warp][s], (n_waits / kDec4Stages) & 1, p.timeout_ns);
+                ++n_waits;
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
                 }
-                __syncthreads();
-                for (int h = warp; h < g; h += kDec4Threads / 32) {
-                    const float x = sc[h][lane];
-                    float mx = x;
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    const float mo = m_run[h], mn = fmaxf(mo, mx);
-                    const float w = lane < cnt ? ex2f(x - mn) : 0.f;
-                    float sum = w;
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                    const float f = mo == -INFINITY ? 0.f : ex2f(mo - mn);
-                    sc[h][lane] = w;
+                uint8_t *ring = sm->ring[warp][s];
+                const int n0 = tile_lo(i), n_keys = tile_n(i);
+                if (has_L && i == n_tiles - 1) {
+                    if (lane < kRow / 16)
+                        reinterpret_cast<uint4 *>(ring + (n_keys - 1) * kRow)[lane] =
+                            reinterpret_cast<const uint4 *>(sm->new_row)[lane];
                     __syncwarp();
-                    if (lane == 0) {
-                        m_run[h] = mn;
-                        l_run[h] = l_run[h] * f + sum;
-                        al[h] = f;
+                }
+#pragma unroll
+                for (int sub = 0; sub < kDec4Tile; sub += 16) {
+                    if (sub >= n_keys) break;
+                    const int ka = sub + dec4_key<HD>(c), kb = ka + 8;  // this lane's keys
+                    const uint8_t *ra = ring + ka * kRow, *rb = ring + kb * kRow;
+                    uint32_t ca[G], cb[G], pa[G], pb[G];  // codes and (s, z) of the two keys
+                    if constexpr (G == 4) {
+                        *reinterpret_cast<uint4 *>(ca) = *reinterpret_cast<const uint4 *>(ra + 16 * r);
+                        *reinterpret_cast<uint4 *>(cb) = *reinterpret_cast<const uint4 *>(rb + 16 * r);
+                        *reinterpret_cast<uint4 *>(pa) = *reinterpret_cast<const uint4 *>(ra + HD);
+                        *reinterpret_cast<uint4 *>(pb) = *reinterpret_cast<const uint4 *>(rb + HD);
+                    } else {
+                        *reinterpret_cast<uint2 *>(ca) = *reinterpret_cast<const uint2 *>(ra + 8 * r);
+                        *reinterpret_cast<uint2 *>(cb) = *reinterpret_cast<const uint2 *>(rb + 8 * r);
+                        *reinterpret_cast<uint2 *>(pa) = *reinterpret_cast<const uint2 *>(ra + HD);
+                        *reinterpret_cast<uint2 *>(pb) = *reinterpret_cast<const uint2 *>(rb + HD);
+                    }
+                    float x[NT][4], xz[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[nt][e] = xz[nt][e] = 0.f;
+                    {
+                        const uint32_t z0a = G == 4 && (r & 1) ? pa[G - 2] : pa[0], z1a = G == 4 && (r & 1) ? pa[G - 1] : pa[1];
+                        const uint32_t z0b = G == 4 && (r & 1) ? pb[G - 2] : pb[0], z1b = G == 4 && (r & 1) ? pb[G - 1] : pb[1];
+                        const uint32_t za = __byte_perm(z0a, z1a, 0x7632), zb = __byte_perm(z0b, z1b, 0x7632);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16_1688(xz[nt], za, zb, qz[nt]);
+                    }
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        float acc[NT][4];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            const uint32_t wa = ca[gr] >> (8 * part), wb = cb[gr] >> (8 * part);
+                            const uint32_t a0 = wa & 0x000f000fu, a2 = wa & 0x00f000f0u;
+                            const uint32_t a1 = wb & 0x000f000fu, a3 = wb & 0x00f000f0u;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_f16_16816(acc[nt], a0, a1, a2, a3, qh[2 * gr + part][nt][0], qh[2 * gr + part][nt][1]);
+                                mma_f16_16816(acc[nt], a0, a1, a2, a3, ql[2 * gr + part][nt][0], ql[2 * gr + part][nt][1]);
+                            }
+                        }
+                        const float sa = lo_f(pa[gr]), sb = lo_f(pb[gr]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            x[nt][0] = fmaf(sa, acc[nt][0], x[nt][0]);
+                            x[nt][1] = fmaf(sa, acc[nt][1], x[nt][1]);
+                            x[nt][2] = fmaf(sb, acc[nt][2], x[nt][2]);
+                            x[nt][3] = fmaf(sb, acc[nt][3], x[nt][3]);
+                        }
+                    }
+                    // ---- scores in log2 units; rows behind the tile's end do not count
+                    const bool va = ka < n_keys, vb = kb < n_keys;
+                    float mx = -INFINITY;  // how far a score lies above the running maximum
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float y = fmaf(x[nt][e], 16777216.f, xz[nt][e]) * x_scale[nt][e & 1];
+                            if (p.alibi) y = fmaf(-slope2[nt][e & 1], static_cast<float>(L - n0 - (e < 2 ? ka : kb)), y);
+                            x[nt][e] = (e < 2 ? va : vb) ? y : -INFINITY;
+                            mx = fmaxf(mx, x[nt][e] - M[nt][e & 1]);
+                        }
+                    // The values' (s, z) of the two keys.
+                    if constexpr (G == 4) {
+                        *reinterpret_cast<uint4 *>(pa) = *reinterpret_cast<const uint4 *>(ra + HD + 4 * G);
+                        *reinterpret_cast<uint4 *>(pb) = *reinterpret_cast<const uint4 *>(rb + HD + 4 * G);
+                    } else {
+                        *reinterpret_cast<uint2 *>(pa) = *reinterpret_cast<const uint2 *>(ra + HD + 4 * G);
+                        *reinterpret_cast<uint2 *>(pb) = *reinterpret_cast<const uint2 *>(rb + HD + 4 * G);
+                    }
+                    if (n_keys < kDec4Tile) {
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) {
+                            if (!va) pa[gr] = 0;
+                            if (!vb) pb[gr] = 0;
+                        }
+                    }
+                    float pr[NT][4];
+                    uint32_t bf[G][NT][2];
+                    auto products = [&] {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) pr[nt][e] = ex2f(x[nt][e] - M[nt][e & 1]);
+                        uint32_t over = 0;
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) {
+                            const float sa = lo_f(pa[gr]) * F[gr], sb = lo_f(pb[gr]) * F[gr];
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                bf[gr][nt][0] = pack_half2(pr[nt][0] * sa, pr[nt][1] * sa);
+                                bf[gr][nt][1] = pack_half2(pr[nt][2] * sb, pr[nt][3] * sb);
+                                const __half2 h = __hmax2(*reinterpret_cast<const __half2 *>(&bf[gr][nt][0]),
+                                                          *reinterpret_cast<const __half2 *>(&bf[gr][nt][1]));
+                                const __half2 t = __hmax2(*reinterpret_cast<const __half2 *>(&top[gr]), h);
+                                top[gr] = *reinterpret_cast<const uint32_t *>(&t);
+                            }
+                            over |= top[gr] + 0x08000800u;  // a half of 2^15 or more sets its top bit
+                        }
+                        return (over & 0x80008000u) != 0;
+                    };
+                    bool redo = mx > 8.f;
+                    uint32_t top_was[G];
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) top_was[gr] = top[gr];
+                    redo |= products();
+                    if (__any_sync(0xffffffffu, redo) || M[0][0] == -INFINITY) {
+                        // Raise the maxima to this tile's and set F anew: the largest product
+                        // so far, of earlier tiles under the new maximum too, goes to 2^12.
+                        float alpha[NT][2], a_max = 0.f;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                float t = fmaxf(x[nt][j], x[nt][j + 2]);
+#pragma unroll
+                                for (int off = 4; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+                                t = fmaxf(t, M[nt][j]);
+                                if (!(fabsf(t) < INFINITY)) t = M[nt][j] == -INFINITY ? 0.f : M[nt][j];
+                                alpha[nt][j] = M[nt][j] == -INFINITY ? 0.f : ex2f(M[nt][j] - t);
+                                M[nt][j] = t;
+                                l[nt][j] *= alpha[nt][j];
+                                a_max = fmaxf(a_max, alpha[nt][j]);
+#pragma unroll
+                                for (int gr = 0; gr < G; ++gr) w[nt][j][gr] *= alpha[nt][j];
+                            }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) pr[nt][e] = ex2f(x[nt][e] - M[nt][e & 1]);
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) {
+                            float t = fmaxf(lo_f(top_was[gr]), hi_f(top_was[gr])) * a_max / F[gr];
+                            const float sa = lo_f(pa[gr]), sb = lo_f(pb[gr]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                t = fmaxf(t, fmaxf(fmaxf(pr[nt][0], pr[nt][1]) * sa, fmaxf(pr[nt][2], pr[nt][3]) * sb));
+#pragma unroll
+                            for (int off = 1; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+                            const float f = pow2i(12 - max(-60, min(60, t > 0.f ? exponent_of(t) : -24)));
+                            const float change = f / F[gr];
+                            F[gr] = f;
+                            top[gr] = pack_half2(t * f, t * f);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    o[gr][0][nt][e] *= alpha[nt][e & 1] * change;
+                                    o[gr][1][nt][e] *= alpha[nt][e & 1] * change;
+                                }
+                        }
+                        products();
+                    }
+                    // ---- sums, and O^T += V^T P
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            l[nt][j] += pr[nt][j] + pr[nt][j + 2];
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr)
+                                w[nt][j][gr] = fmaf(pr[nt][j], hi_f(pa[gr]), fmaf(pr[nt][j + 2], hi_f(pb[gr]), w[nt][j][gr]));
+                        }
+                    uint32_t vw[4][G / 2];  // value words of the four keys of this lane's k indices
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint8_t *row = ring + (sub + dec4_key<HD>((k >> 1) * 8 + 2 * r + (k & 1))) * kRow + HD / 2;
+                        if constexpr (G == 4)
+                            *reinterpret_cast<uint2 *>(vw[k]) = *reinterpret_cast<const uint2 *>(row + 8 * c);
+                        else
+                            vw[k][0] = *reinterpret_cast<const uint32_t *>(row + 4 * c);
+                    }
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        const uint32_t sel = gr & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t u = __byte_perm(vw[0][gr / 2], vw[1][gr / 2], sel);
+                        const uint32_t t = __byte_perm(vw[2][gr / 2], vw[3][gr / 2], sel);
+                        uint32_t b0[NT], b1[NT];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            b0[nt] = movm_t(bf[gr][nt][0]);
+                            b1[nt] = movm_t(bf[gr][nt][1]);
+                        }
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t us = u >> (8 * m), ts = t >> (8 * m);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16_16816(o[gr][m][nt], us & 0x000f000fu, us & 0x00f000f0u,
+                                              ts & 0x000f000fu, ts & 0x00f000f0u, b0[nt], b1[nt]);
+                        }
                     }
                 }
-                __syncthreads();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int h = j * (kDec4Threads / HD) + tid / HD;
-                    if (h >= g) continue;
-                    float s = acc[j] * al[h];
-                    for (int r = 0; r < cnt; ++r) s = fmaf(sc[h][r], v[r][dim], s);
-                    acc[j] = s;
-                }
+                __syncwarp();  // the whole warp is done with the stage
+                const int nxt = i + kDec4Stages * kDec4Warps;
+                if (nxt < n_tiles) load(nxt);
             }
+
+            // ---- the warps' results: outputs of head h, dims, in place of the ring
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) {
+                        l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr)
+                            w[nt][j][gr] += __shfl_xor_sync(0xffffffffu, w[nt][j][gr], off);
+                    }
+                    if (lane < 4) {
+                        sm->m[warp][nt * 8 + 2 * r + j] = M[nt][j];
+                        sm->l[warp][nt * 8 + 2 * r + j] = l[nt][j];
+                    }
+                }
+            if (!ok) {  // a copy did not land: no partial result to trust
+                raise_status(kStatusTimeoutDecode);
+                sm->abort = 1;
+                for (; n_waits < n_loads; ++n_waits)  // the copies still under way
+                    mbar_wait_drain(&sm->full[warp][n_waits % kDec4Stages],
+                                    (n_waits / kDec4Stages) & 1, p.timeout_ns);
+            }
+            __syncthreads();
+            if (sm->abort) return;
+            float *red = reinterpret_cast<float *>(&sm->ring[0][0][0]);  // [warps][8 NT][HD]
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                const float f = 1.f / F[gr];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float add = w[nt][j][gr];
+                        const float4 out = make_float4(fmaf(o[gr][0][nt][j], 16777216.f * f, add),
+                                                       fmaf(o[gr][0][nt][j + 2], 1048576.f * f, add),
+                                                       fmaf(o[gr][1][nt][j], 16777216.f * f, add),
+                                                       fmaf(o[gr][1][nt][j + 2], 1048576.f * f, add));
+                        *reinterpret_cast<float4 *>(red + (warp * 8 * NT + nt * 8 + 2 * r + j) * HD + 32 * gr + 4 * c) = out;
+                    }
+            }
+            __syncthreads();
             const long long slot = (blockIdx.x + static_cast<long long>(b) * p.Hkv + kvh) * g;
+            for (int i = tid; i < g * HD; i += kDec4Threads) {
+                const int h = i / HD, dim = i % HD;
+                float top_m = -INFINITY, acc = 0.f, sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int h = j * (kDec4Threads / HD) + tid / HD;
-                if (h >= g) continue;
-                p.ws_o[(slot + h) * HD + dim] = acc[j];
+                for (int k = 0; k < kDec4Warps; ++k) top_m = fmaxf(top_m, sm->m[k][h]);
+#pragma unroll
+                for (int k = 0; k < kDec4Warps; ++k) {
+                    const float f = sm->m[k][h] == -INFINITY ? 0.f : ex2f(sm->m[k][h] - top_m);
+                    acc += f * red[(k * 8 * NT + h) * HD + dim];
+                    sum += f * sm->l[k][h];
+                }
+                p.ws_o[(slot + h) * HD + dim] = acc;
                 if (dim == 0) {
-                    p.ws_ml[(slot + h) * 2] = m_run[h];
-                    p.ws_ml[(slot + h) * 2 + 1] = l_run[h];
+                    p.ws_ml[(slot + h) * 2] = top_m;
+                    p.ws_ml[(slot + h) * 2 + 1] = sum;
                 }
             }
+            fence_proxy_async_smem();  // the ring's next copies follow these writes and reads
+            __syncthreads();
         }
     }
 }

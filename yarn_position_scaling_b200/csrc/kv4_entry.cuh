@@ -94,6 +94,30 @@ size_t decode4_ws_bytes(long long B, long long Hq, long long Hkv, long long d) {
     return static_cast<size_t>((yr::kDec4MaxBlocks + B * Hkv) * (Hq / Hkv) * (d + 2) * 4);
 }
 
+// One wave of the split kernel, and the places of its partial results.
+template <int HD, int NT, bool kHalf>
+int launch_decode4(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
+    static int per_sm = 0;  // same value on every device of this build's target
+    if (per_sm == 0) {
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                &n, yr::decode4_split_kernel<HD, NT, kHalf>, yr::kDec4Threads,
+                yr::decode4_smem_bytes<HD, NT>()) != cudaSuccess ||
+            n < 1)
+            n = 1;
+        per_sm = n;
+    }
+    const int blocks = per_sm * sm_count;
+    dp.grid_blocks = blocks < yr::kDec4MaxBlocks ? blocks : yr::kDec4MaxBlocks;
+    const long long slots = dp.grid_blocks + static_cast<long long>(dp.B) * dp.Hkv;
+    dp.ws_ml = dp.ws_o + slots * dp.group * HD;
+    yr::decode4_split_kernel<HD, NT, kHalf>
+        <<<dp.grid_blocks, yr::kDec4Threads, yr::decode4_smem_bytes<HD, NT>(), st>>>(dp);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail("decode4_split_kernel launch", e);
+    return YR_OK;
+}
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace yr_host
@@ -221,27 +245,26 @@ extern "C" int yr_attn_decode_kv4(const void *q_new, const void *k_new, const vo
     dp.sl2 = static_cast<float>(tab->softmax_scale * 1.4426950408889634);
     dp.alibi = tab->method == YR_ALIBI ? 1 : 0;
     for (int i = 0; i < d / 2; ++i) dp.turns[i] = tab->turns[i];
-    dp.grid_blocks = 4 * sm_count < yr::kDec4MaxBlocks ? 4 * sm_count : yr::kDec4MaxBlocks;
-    const long long slots = dp.grid_blocks + static_cast<long long>(B) * Hkv;
+    dp.timeout_ns = wait_timeout_ns();
     dp.ws_o = static_cast<float *>(workspace);
-    dp.ws_ml = dp.ws_o + slots * g * d;
     const bool half = tab->pairs == YR_PAIR_HALF;
-    if (d == 128 && half)
-        yr::decode4_split_kernel<128, true><<<dp.grid_blocks, yr::kDec4Threads, 0, st>>>(dp);
-    else if (d == 128)
-        yr::decode4_split_kernel<128, false><<<dp.grid_blocks, yr::kDec4Threads, 0, st>>>(dp);
-    else if (half)
-        yr::decode4_split_kernel<64, true><<<dp.grid_blocks, yr::kDec4Threads, 0, st>>>(dp);
+    if (d == 128)
+        rc = g <= 8 ? half ? launch_decode4<128, 1, true>(dp, sm_count, st)
+                           : launch_decode4<128, 1, false>(dp, sm_count, st)
+             : half ? launch_decode4<128, 2, true>(dp, sm_count, st)
+                    : launch_decode4<128, 2, false>(dp, sm_count, st);
     else
-        yr::decode4_split_kernel<64, false><<<dp.grid_blocks, yr::kDec4Threads, 0, st>>>(dp);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail("decode4_split_kernel launch", e);
+        rc = g <= 8 ? half ? launch_decode4<64, 1, true>(dp, sm_count, st)
+                           : launch_decode4<64, 1, false>(dp, sm_count, st)
+             : half ? launch_decode4<64, 2, true>(dp, sm_count, st)
+                    : launch_decode4<64, 2, false>(dp, sm_count, st);
+    if (rc != YR_OK) return rc;
     const unsigned merge = static_cast<unsigned>(B) * Hq;
     if (d == 128)
         yr::decode4_merge_kernel<128><<<merge, 128, 0, st>>>(dp);
     else
         yr::decode4_merge_kernel<64><<<merge, 64, 0, st>>>(dp);
-    e = cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("decode4_merge_kernel launch", e);
     return YR_OK;
 }

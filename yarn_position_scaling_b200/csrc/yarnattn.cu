@@ -152,6 +152,22 @@ int prepare_device(int *sm_count, DeviceState *out = nullptr) {
                  yr::decode_smem_bytes<64>()},
                 {reinterpret_cast<const void *>(&yr::decode_split_kernel<64, 2>),
                  yr::decode_smem_bytes<64>()},
+                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<128, 1, false>),
+                 yr::decode4_smem_bytes<128, 1>()},
+                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<128, 1, true>),
+                 yr::decode4_smem_bytes<128, 1>()},
+                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<128, 2, false>),
+                 yr::decode4_smem_bytes<128, 2>()},
+                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<128, 2, true>),
+                 yr::decode4_smem_bytes<128, 2>()},
+                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<64, 1, false>),
+                 yr::decode4_smem_bytes<64, 1>()},
+                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<64, 1, true>),
+                 yr::decode4_smem_bytes<64, 1>()},
+                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<64, 2, false>),
+                 yr::decode4_smem_bytes<64, 2>()},
+                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<64, 2, true>),
+                 yr::decode4_smem_bytes<64, 2>()},
             };
             for (auto &a : attrs) {
                 e = cudaFuncSetAttribute(a.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -978,6 +994,7 @@ extern "C" int yr_device_status(void *stream) {
     if (v & yr::kStatusTimeoutMma) msg += " prefill-mma-timeout";
     if (v & yr::kStatusTimeoutSoftmax) msg += " prefill-softmax-timeout";
     if (v & yr::kStatusTimeoutDrain) msg += " prefill-drain-timeout";
+    if (v & yr::kStatusTimeoutDecode) msg += " decode-load-timeout";
     if (v & yr::kStatusBadCacheLen) msg += " decode-cache-length-out-of-range";
     if (v & yr::kStatusRange)
         msg += " prefill-operand-outside-fp16-range (|rotated q|, |rotated k| or |v| >= 65520,"

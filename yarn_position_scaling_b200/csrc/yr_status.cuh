@@ -9,6 +9,7 @@ enum StatusBits : unsigned {
     kStatusTimeoutMma = 1u << 1,      // prefill MMA issuer gave up waiting
     kStatusTimeoutSoftmax = 1u << 2,  // prefill softmax warps gave up waiting
     kStatusTimeoutDrain = 1u << 3,    // prefill teardown gave up draining copies/MMAs
+    kStatusTimeoutDecode = 1u << 4,   // 4-bit decode gave up waiting for a copy
     kStatusBadCacheLen = 1u << 8,     // a cache length or row range outside the cache
     kStatusRange = 1u << 9,           // prefill: an operand outside the fp16 range (|x| >= 65520,
                                       // or not a number) after rotation or conversion
