@@ -15,6 +15,7 @@
 namespace yr {
 
 constexpr int kDec4Chunk = 128;      // least keys per block: a tile for each warp
+constexpr int kDec4Lead = 256;       // what a segment costs besides its keys, in keys
 constexpr int kDec4MaxBlocks = 640;  // most blocks of the split launch
 constexpr int kDec4Warps = 4;
 constexpr int kDec4Threads = kDec4Warps * 32;
@@ -57,20 +58,19 @@ __device__ __forceinline__ DecRanges dec4_ranges(const Decode4Params &p, int L) 
     return r;
 }
 
-// The partition, as every block derives it from cache_len: total keys, and the first
-// sequence that reaches beyond unit `u` with the units before it.  Called by a full warp.
-struct Dec4Plan {
-    long long total, before;
-    int b;
-};
+// The partition, as every block derives it from cache_len.  A segment is kDec4Lead units
+// for what a block does once for it (query, partial result) and one for each key, so that
+// blocks of many short segments and blocks of few long ones take equally long.
 __device__ __forceinline__ long long dec4_units_per_block(const Decode4Params &p, long long total) {
     const long long even = (total + p.grid_blocks - 1) / p.grid_blocks;
-    return even > kDec4Chunk ? even : kDec4Chunk;
+    return even > kDec4Chunk + kDec4Lead ? even : kDec4Chunk + kDec4Lead;
 }
+// Units of a segment with `keys` visible keys: none for a length outside the cache.
+__device__ __forceinline__ long long dec4_seg_units(long long keys) { return keys > 0 ? keys + kDec4Lead : 0; }
 __device__ __forceinline__ long long dec4_seq_units(const Decode4Params &p, int b) {
     if (b >= p.B) return 0;
     const DecRanges r = dec4_ranges(p, p.cache_len[b]);
-    return static_cast<long long>(p.Hkv) * (r.len1 + r.len2);
+    return p.Hkv * dec4_seg_units(static_cast<long long>(r.len1) + r.len2);
 }
 __device__ __forceinline__ long long dec4_total(const Decode4Params &p, int lane) {
     long long t = 0;
@@ -114,18 +114,29 @@ __device__ __forceinline__ void dec4_append(const Decode4Params &p, int b, int k
 // ---------------------------------------------------------------------------- fragments
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_f16_1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b0));
+// The same with a zero accumulator to begin with.
+__device__ __forceinline__ void mma0_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma0_f16_1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+        "{%7,%7,%7,%7};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar,
                                           uint64_t policy) {
@@ -163,8 +174,9 @@ struct Decode4Smem {
     alignas(128) uint8_t ring[kDec4Warps][kDec4Stages][kStageBytes];  // also the warps' outputs
     alignas(16) uint8_t new_row[kv4_row_bytes(HD)];
     double2 cs[HD / 2];
-    float q[8 * NT][HD];
-    float q_scale[8 * NT];  // the power of two that the head's query was multiplied by
+    uint4 q_hi[8 * NT][HD / 8], q_lo[8 * NT][HD / 8];  // fragments, see the rotation below
+    float q_sum[8 * NT][HD / kKv4Group];  // sums of the scaled query over the groups
+    float q_scale[8 * NT];  // what takes the scaled query back
     float m[kDec4Warps][8 * NT], l[kDec4Warps][8 * NT];
     uint64_t full[kDec4Warps][kDec4Stages];
     int abort;
@@ -183,10 +195,10 @@ constexpr size_t decode4_smem_bytes() {
 //   and exact.  The query is split into two fp16 parts.  Each 32-element group has its own
 //   accumulator, multiplied by the row's s in fp32; z (sum of q over the group) is one more
 //   product of fp16 operands, again with the sum in two parts.
-//   Outputs: O^T[16 dims x 8 heads], value codes as A in the same way, B = p s F with a
-//   power of two F per group that keeps it between fp16's ends; sum p z in fp32.
-//   The running maximum is raised only when a score passes it by 2^8, and F is changed only
-//   then or when a product nears overflow, so the common tile costs one vote.
+//   Outputs: O^T[16 dims x 8 heads], value codes as A in the same way, B = p s in fp16; sum
+//   p z in fp32.  p = 2^(score - R) for a reference R per head that puts the largest p s of
+//   a tile at 2^12 and is raised only once one passes 2^15: small scales keep their bits
+//   (fp16 holds 2^-14 at full precision), and the common tile costs one vote.
 template <int HD, int NT, bool kHalf>
 __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
     decode4_split_kernel(const __grid_constant__ Decode4Params p) {
@@ -223,21 +235,23 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
     for (; b < p.B && seg0 < u_hi; ++b) {
         const int L = p.cache_len[b];
         const DecRanges rg = dec4_ranges(p, L);
-        const long long V = rg.len1 + rg.len2;
+        const long long V = dec4_seg_units(static_cast<long long>(rg.len1) + rg.len2);
         if (V == 0) continue;
         int kvh = seg0 < u_lo ? static_cast<int>((u_lo - seg0) / V) : 0;
         seg0 += kvh * V;
         for (; kvh < p.Hkv && seg0 < u_hi; ++kvh, seg0 += V) {
-            // Units [u0, u1) of the segment are this block's: keys of the first range, then
-            // of the second.
-            const int u0 = static_cast<int>(max(u_lo, seg0) - seg0);
-            const int u1 = static_cast<int>(min(u_hi, seg0 + V) - seg0);
+            // Units [u0, u1) of the segment's keys are this block's: keys of the first
+            // range, then of the second.
+            const long long k0 = seg0 + kDec4Lead;
+            const int u0 = static_cast<int>(max(u_lo, k0) - k0);
+            const int u1 = static_cast<int>(min(u_hi, seg0 + V) - k0);
+            if (u1 <= 0) continue;
             const int lo1 = min(u0, rg.len1), hi1 = min(u1, rg.len1);
             const int lo2 = rg.lo2 + max(u0, rg.len1) - rg.len1;
             const int hi2 = rg.lo2 + max(u1, rg.len1) - rg.len1;
             const int n_t1 = (hi1 - lo1 + kDec4Tile - 1) / kDec4Tile;
             const int n_tiles = n_t1 + (hi2 - lo2 + kDec4Tile - 1) / kDec4Tile;
-            const bool has_L = u1 == V;  // the new row is the last of this block's keys
+            const bool has_L = u1 == rg.len1 + rg.len2;  // the new row is the last of this block's keys
             uint8_t *plane = p.kv4 + (static_cast<long long>(b) * p.Hkv + kvh) * p.T_max * kRow;
             auto tile_lo = [&](int i) { return i < n_t1 ? lo1 + i * kDec4Tile : lo2 + (i - n_t1) * kDec4Tile; };
             auto tile_n = [&](int i) { return min(kDec4Tile, (i < n_t1 ? hi1 : hi2) - tile_lo(i)); };
@@ -275,8 +289,25 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                 // and the second part keeps its bits.
                 const int e2 = mx > 0.f ? max(-100, min(127, exponent_of(mx))) : 0;
                 const float f = pow2i(7 - e2);
+                // The fragment words of lane r = ch % 4 for group ch / 4: word 2 part + k
+                // holds elements 2 part + k and, above it, 4 further on; those of k = 1 meet
+                // codes of the byte's upper half and are scaled by 2^-4.
+                uint32_t hi[4], lo[4];
+                float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sm->q[h][8 * ch + e] = y[e] * f;
+                for (int e = 0; e < 4; ++e) {
+                    const float v0 = y[e] * f, v1 = y[e + 4] * f;
+                    sum += v0 + v1;
+                    const float t0 = e & 1 ? v0 * 0.0625f : v0, t1 = e & 1 ? v1 * 0.0625f : v1;
+                    const __half2 hv = __floats2half2_rn(t0, t1);
+                    hi[e] = *reinterpret_cast<const uint32_t *>(&hv);
+                    lo[e] = pack_half2(t0 - __low2float(hv), t1 - __high2float(hv));
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sm->q_hi[h][ch] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                sm->q_lo[h][ch] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if ((ch & 3) == 0) sm->q_sum[h][ch >> 2] = sum;
                 if (ch == 0) sm->q_scale[h] = pow2i(e2 - 7);
             }
             const int last_warp = (n_tiles - 1) % kDec4Warps;
@@ -289,57 +320,47 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
             }
             __syncthreads();
             uint32_t qh[2 * G][NT][2], ql[2 * G][NT][2], qz[NT];
-            float x_scale[NT][2], slope2[NT][2];
+            float x_scale[NT][2], slope[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float *q = sm->q[nt * 8 + c];
-                float zs[2] = {0.f, 0.f};  // group sums of this lane's part of the z product
+                const int h = nt * 8 + c;
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int at = 32 * gr + 8 * r + 2 * part + k;
-                            const float f = k == 0 ? 1.f : 0.0625f;
-                            const float v0 = q[at] * f, v1 = q[at + 4] * f;
-                            const __half h0 = __float2half_rn(v0), h1 = __float2half_rn(v1);
-                            const __half2 hv = __halves2half2(h0, h1);
-                            qh[2 * gr + part][nt][k] = *reinterpret_cast<const uint32_t *>(&hv);
-                            ql[2 * gr + part][nt][k] = pack_half2(v0 - __half2float(h0), v1 - __half2float(h1));
-                        }
-                    if (gr / 2 == (r & 1)) {
-                        float s = 0.f;
-                        for (int j = 0; j < 32; ++j) s += q[32 * gr + j];
-                        zs[gr & 1] = s;
-                    }
+                    const uint4 hi = sm->q_hi[h][4 * gr + r], lo = sm->q_lo[h][4 * gr + r];
+                    qh[2 * gr][nt][0] = hi.x;
+                    qh[2 * gr][nt][1] = hi.y;
+                    qh[2 * gr + 1][nt][0] = hi.z;
+                    qh[2 * gr + 1][nt][1] = hi.w;
+                    ql[2 * gr][nt][0] = lo.x;
+                    ql[2 * gr][nt][1] = lo.y;
+                    ql[2 * gr + 1][nt][0] = lo.z;
+                    ql[2 * gr + 1][nt][1] = lo.w;
                 }
-                const __half h0 = __float2half_rn(zs[0]), h1 = __float2half_rn(zs[1]);
-                const __half2 hv = __halves2half2(h0, h1);
+                // The z product: k = 2r, 2r+1 stand for the sums' first parts of the groups
+                // 2r, 2r+1 (r < 2) and for their second parts (r >= 2).
+                const int g0 = 2 * (r & 1);
+                const float z0 = g0 < G ? sm->q_sum[h][g0] : 0.f, z1 = g0 < G ? sm->q_sum[h][g0 + 1] : 0.f;
+                const __half2 hv = __floats2half2_rn(z0, z1);
                 qz[nt] = r < 2 ? *reinterpret_cast<const uint32_t *>(&hv)
-                               : pack_half2(zs[0] - __half2float(h0), zs[1] - __half2float(h1));
+                               : pack_half2(z0 - __low2float(hv), z1 - __high2float(hv));
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int col = nt * 8 + 2 * r + j;
                     x_scale[nt][j] = p.sl2 * sm->q_scale[col];
-                    slope2[nt][j] = p.alibi ? exp2f(-8.0f * static_cast<float>(kvh * g + col + 1) /
-                                                    static_cast<float>(p.Hq)) * 1.4426950408889634f
-                                            : 0.f;
+                    // The bias m (L - n) in units of x, before x_scale.
+                    slope[nt][j] = p.alibi ? exp2f(-8.0f * static_cast<float>(kvh * g + col + 1) /
+                                                   static_cast<float>(p.Hq)) * 1.4426950408889634f /
+                                                 x_scale[nt][j]
+                                           : 0.f;
                 }
             }
 
-            float o[G][2][NT][4], w[NT][2][G], l[NT][2], M[NT][2], F[G];
-            uint32_t top[G];  // largest B operand of each group so far, per head parity
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                F[gr] = 1.f;
-                top[gr] = 0;
-            }
+            float o[G][2][NT][4], w[NT][2][G], l[NT][2], R[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    M[nt][j] = -INFINITY;
+                    R[nt][j] = -INFINITY;
                     l[nt][j] = 0.f;
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
@@ -365,7 +386,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                             reinterpret_cast<const uint4 *>(sm->new_row)[lane];
                     __syncwarp();
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int sub = 0; sub < kDec4Tile; sub += 16) {
                     if (sub >= n_keys) break;
                     const int ka = sub + dec4_key<HD>(c), kb = ka + 8;  // this lane's keys
@@ -383,24 +404,17 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                         *reinterpret_cast<uint2 *>(pb) = *reinterpret_cast<const uint2 *>(rb + HD);
                     }
                     float x[NT][4], xz[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[nt][e] = xz[nt][e] = 0.f;
                     {
-                        const uint32_t z0a = G == 4 && (r & 1) ? pa[G - 2] : pa[0], z1a = G == 4 && (r & 1) ? pa[G - 1] : pa[1];
-                        const uint32_t z0b = G == 4 && (r & 1) ? pb[G - 2] : pb[0], z1b = G == 4 && (r & 1) ? pb[G - 1] : pb[1];
-                        const uint32_t za = __byte_perm(z0a, z1a, 0x7632), zb = __byte_perm(z0b, z1b, 0x7632);
+                        const int at = HD + (G == 4 ? 8 * (r & 1) : 0);
+                        const uint2 wa = *reinterpret_cast<const uint2 *>(ra + at);
+                        const uint2 wb = *reinterpret_cast<const uint2 *>(rb + at);
+                        const uint32_t za = __byte_perm(wa.x, wa.y, 0x7632), zb = __byte_perm(wb.x, wb.y, 0x7632);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16_1688(xz[nt], za, zb, qz[nt]);
+                        for (int nt = 0; nt < NT; ++nt) mma0_f16_1688(xz[nt], za, zb, qz[nt]);
                     }
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
                         float acc[NT][4];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
 #pragma unroll
                         for (int part = 0; part < 2; ++part) {
                             const uint32_t wa = ca[gr] >> (8 * part), wb = cb[gr] >> (8 * part);
@@ -408,32 +422,27 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                             const uint32_t a1 = wb & 0x000f000fu, a3 = wb & 0x00f000f0u;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                mma_f16_16816(acc[nt], a0, a1, a2, a3, qh[2 * gr + part][nt][0], qh[2 * gr + part][nt][1]);
+                                if (part == 0)
+                                    mma0_f16_16816(acc[nt], a0, a1, a2, a3, qh[2 * gr][nt][0], qh[2 * gr][nt][1]);
+                                else
+                                    mma_f16_16816(acc[nt], a0, a1, a2, a3, qh[2 * gr + 1][nt][0], qh[2 * gr + 1][nt][1]);
                                 mma_f16_16816(acc[nt], a0, a1, a2, a3, ql[2 * gr + part][nt][0], ql[2 * gr + part][nt][1]);
                             }
                         }
                         const float sa = lo_f(pa[gr]), sb = lo_f(pb[gr]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            x[nt][0] = fmaf(sa, acc[nt][0], x[nt][0]);
-                            x[nt][1] = fmaf(sa, acc[nt][1], x[nt][1]);
-                            x[nt][2] = fmaf(sb, acc[nt][2], x[nt][2]);
-                            x[nt][3] = fmaf(sb, acc[nt][3], x[nt][3]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[nt][e] = gr == 0 ? (e < 2 ? sa : sb) * acc[nt][e]
+                                                   : fmaf(e < 2 ? sa : sb, acc[nt][e], x[nt][e]);
                         }
                     }
-                    // ---- scores in log2 units; rows behind the tile's end do not count
-                    const bool va = ka < n_keys, vb = kb < n_keys;
-                    float mx = -INFINITY;  // how far a score lies above the running maximum
+                    // ---- scores over x_scale; then the values' (s, z) of the two keys
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float y = fmaf(x[nt][e], 16777216.f, xz[nt][e]) * x_scale[nt][e & 1];
-                            if (p.alibi) y = fmaf(-slope2[nt][e & 1], static_cast<float>(L - n0 - (e < 2 ? ka : kb)), y);
-                            x[nt][e] = (e < 2 ? va : vb) ? y : -INFINITY;
-                            mx = fmaxf(mx, x[nt][e] - M[nt][e & 1]);
-                        }
-                    // The values' (s, z) of the two keys.
+                        for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(x[nt][e], 16777216.f, xz[nt][e]);
                     if constexpr (G == 4) {
                         *reinterpret_cast<uint4 *>(pa) = *reinterpret_cast<const uint4 *>(ra + HD + 4 * G);
                         *reinterpret_cast<uint4 *>(pb) = *reinterpret_cast<const uint4 *>(rb + HD + 4 * G);
@@ -441,87 +450,85 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                         *reinterpret_cast<uint2 *>(pa) = *reinterpret_cast<const uint2 *>(ra + HD + 4 * G);
                         *reinterpret_cast<uint2 *>(pb) = *reinterpret_cast<const uint2 *>(rb + HD + 4 * G);
                     }
-                    if (n_keys < kDec4Tile) {
+                    if (p.alibi) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[nt][e] = fmaf(-slope[nt][e & 1], static_cast<float>(L - n0 - (e < 2 ? ka : kb)), x[nt][e]);
+                    }
+                    if (n_keys < kDec4Tile) {  // rows behind the tile's end do not count
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if ((e < 2 ? ka : kb) >= n_keys) x[nt][e] = -INFINITY;
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
-                            if (!va) pa[gr] = 0;
-                            if (!vb) pb[gr] = 0;
+                            if (ka >= n_keys) pa[gr] = 0;
+                            if (kb >= n_keys) pb[gr] = 0;
                         }
                     }
                     float pr[NT][4];
                     uint32_t bf[G][NT][2];
+                    // Probabilities and B operands; true if one of the latter nears fp16's end
+                    // (or would, but for a scale of 0).
                     auto products = [&] {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) pr[nt][e] = ex2f(x[nt][e] - M[nt][e & 1]);
-                        uint32_t over = 0;
+                            for (int e = 0; e < 4; ++e) pr[nt][e] = ex2f(fmaf(x[nt][e], x_scale[nt][e & 1], -R[nt][e & 1]));
+                        float p_max = 0.f;
+                        __half2 t = __half2half2(__ushort_as_half(0));
 #pragma unroll
                         for (int gr = 0; gr < G; ++gr) {
-                            const float sa = lo_f(pa[gr]) * F[gr], sb = lo_f(pb[gr]) * F[gr];
+                            const float sa = lo_f(pa[gr]), sb = lo_f(pb[gr]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 bf[gr][nt][0] = pack_half2(pr[nt][0] * sa, pr[nt][1] * sa);
                                 bf[gr][nt][1] = pack_half2(pr[nt][2] * sb, pr[nt][3] * sb);
-                                const __half2 h = __hmax2(*reinterpret_cast<const __half2 *>(&bf[gr][nt][0]),
-                                                          *reinterpret_cast<const __half2 *>(&bf[gr][nt][1]));
-                                const __half2 t = __hmax2(*reinterpret_cast<const __half2 *>(&top[gr]), h);
-                                top[gr] = *reinterpret_cast<const uint32_t *>(&t);
+                                t = __hmax2(t, *reinterpret_cast<const __half2 *>(&bf[gr][nt][0]));
+                                t = __hmax2(t, *reinterpret_cast<const __half2 *>(&bf[gr][nt][1]));
                             }
-                            over |= top[gr] + 0x08000800u;  // a half of 2^15 or more sets its top bit
                         }
-                        return (over & 0x80008000u) != 0;
-                    };
-                    bool redo = mx > 8.f;
-                    uint32_t top_was[G];
 #pragma unroll
-                    for (int gr = 0; gr < G; ++gr) top_was[gr] = top[gr];
-                    redo |= products();
-                    if (__any_sync(0xffffffffu, redo) || M[0][0] == -INFINITY) {
-                        // Raise the maxima to this tile's and set F anew: the largest product
-                        // so far, of earlier tiles under the new maximum too, goes to 2^12.
-                        float alpha[NT][2], a_max = 0.f;
+                        for (int nt = 0; nt < NT; ++nt)
+                            p_max = fmaxf(p_max, fmaxf(fmaxf(pr[nt][0], pr[nt][1]), fmaxf(pr[nt][2], pr[nt][3])));
+                        const uint32_t largest = *reinterpret_cast<const uint32_t *>(&t);
+                        return ((largest + 0x08000800u) & 0x80008000u) != 0 || p_max > 1.1e12f;
+                    };
+                    if (__any_sync(0xffffffffu, products())) {
+                        // Raise the references to these keys' largest p s, put at 2^12 (a scale
+                        // below fp16's smallest counts as that).
+                        float sa = 0.f, sb = 0.f;
+#pragma unroll
+                        for (int gr = 0; gr < G; ++gr) {
+                            sa = fmaxf(sa, lo_f(pa[gr]));
+                            sb = fmaxf(sb, lo_f(pb[gr]));
+                        }
+                        sa = log2f(fmaxf(sa, 5.9604645e-8f)) - 12.f;
+                        sb = log2f(fmaxf(sb, 5.9604645e-8f)) - 12.f;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                float t = fmaxf(x[nt][j], x[nt][j + 2]);
+                                float t = fmaxf(fmaf(x[nt][j], x_scale[nt][j], sa), fmaf(x[nt][j + 2], x_scale[nt][j], sb));
 #pragma unroll
                                 for (int off = 4; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-                                t = fmaxf(t, M[nt][j]);
-                                if (!(fabsf(t) < INFINITY)) t = M[nt][j] == -INFINITY ? 0.f : M[nt][j];
-                                alpha[nt][j] = M[nt][j] == -INFINITY ? 0.f : ex2f(M[nt][j] - t);
-                                M[nt][j] = t;
-                                l[nt][j] *= alpha[nt][j];
-                                a_max = fmaxf(a_max, alpha[nt][j]);
+                                t = fmaxf(t, R[nt][j]);
+                                if (!(fabsf(t) < INFINITY)) t = R[nt][j] == -INFINITY ? 0.f : R[nt][j];
+                                const float f = R[nt][j] == -INFINITY ? 0.f : ex2f(R[nt][j] - t);
+                                R[nt][j] = t;
+                                l[nt][j] *= f;
 #pragma unroll
-                                for (int gr = 0; gr < G; ++gr) w[nt][j][gr] *= alpha[nt][j];
-                            }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) pr[nt][e] = ex2f(x[nt][e] - M[nt][e & 1]);
-#pragma unroll
-                        for (int gr = 0; gr < G; ++gr) {
-                            float t = fmaxf(lo_f(top_was[gr]), hi_f(top_was[gr])) * a_max / F[gr];
-                            const float sa = lo_f(pa[gr]), sb = lo_f(pb[gr]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                t = fmaxf(t, fmaxf(fmaxf(pr[nt][0], pr[nt][1]) * sa, fmaxf(pr[nt][2], pr[nt][3]) * sb));
-#pragma unroll
-                            for (int off = 1; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-                            const float f = pow2i(12 - max(-60, min(60, t > 0.f ? exponent_of(t) : -24)));
-                            const float change = f / F[gr];
-                            F[gr] = f;
-                            top[gr] = pack_half2(t * f, t * f);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    o[gr][0][nt][e] *= alpha[nt][e & 1] * change;
-                                    o[gr][1][nt][e] *= alpha[nt][e & 1] * change;
+                                for (int gr = 0; gr < G; ++gr) {
+                                    w[nt][j][gr] *= f;
+                                    o[gr][0][nt][j] *= f;
+                                    o[gr][0][nt][j + 2] *= f;
+                                    o[gr][1][nt][j] *= f;
+                                    o[gr][1][nt][j + 2] *= f;
                                 }
-                        }
+                            }
                         products();
                     }
                     // ---- sums, and O^T += V^T P
@@ -551,8 +558,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                         uint32_t b0[NT], b1[NT];
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            b0[nt] = movm_t(bf[gr][nt][0]);
-                            b1[nt] = movm_t(bf[gr][nt][1]);
+                            b0[nt] = transpose8(bf[gr][nt][0]);
+                            b1[nt] = transpose8(bf[gr][nt][1]);
                         }
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
@@ -582,7 +589,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                             w[nt][j][gr] += __shfl_xor_sync(0xffffffffu, w[nt][j][gr], off);
                     }
                     if (lane < 4) {
-                        sm->m[warp][nt * 8 + 2 * r + j] = M[nt][j];
+                        sm->m[warp][nt * 8 + 2 * r + j] = R[nt][j];
                         sm->l[warp][nt * 8 + 2 * r + j] = l[nt][j];
                     }
                 }
@@ -598,16 +605,15 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
             float *red = reinterpret_cast<float *>(&sm->ring[0][0][0]);  // [warps][8 NT][HD]
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
-                const float f = 1.f / F[gr];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float add = w[nt][j][gr];
-                        const float4 out = make_float4(fmaf(o[gr][0][nt][j], 16777216.f * f, add),
-                                                       fmaf(o[gr][0][nt][j + 2], 1048576.f * f, add),
-                                                       fmaf(o[gr][1][nt][j], 16777216.f * f, add),
-                                                       fmaf(o[gr][1][nt][j + 2], 1048576.f * f, add));
+                        const float4 out = make_float4(fmaf(o[gr][0][nt][j], 16777216.f, add),
+                                                       fmaf(o[gr][0][nt][j + 2], 1048576.f, add),
+                                                       fmaf(o[gr][1][nt][j], 16777216.f, add),
+                                                       fmaf(o[gr][1][nt][j + 2], 1048576.f, add));
                         *reinterpret_cast<float4 *>(red + (warp * 8 * NT + nt * 8 + 2 * r + j) * HD + 32 * gr + 4 * c) = out;
                     }
             }
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(HD) decode4_merge_kernel(const __grid_constant
     const int L = p.cache_len[b], g = p.group, kvh = hq / g, hh = hq % g;
     const long long oi = static_cast<long long>(b) * p.Hq + hq;
     const DecRanges rg = dec4_ranges(p, L);
-    const long long V = rg.len1 + rg.len2;
+    const long long V = dec4_seg_units(static_cast<long long>(rg.len1) + rg.len2);
     if (V == 0) {  // a length outside the cache
         p.o[oi * HD + dim] = __float2bfloat16(__int_as_float(0x7fc00000));
         if (p.lse != nullptr && dim == 0) p.lse[oi] = __int_as_float(0x7fc00000);
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(HD) decode4_merge_kernel(const __grid_constant
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) seg0 += __shfl_xor_sync(0xffffffffu, seg0, off);
     seg0 += kvh * V;
-    const int first = static_cast<int>(seg0 / U), last = static_cast<int>((seg0 + V - 1) / U);
+    const int first = static_cast<int>((seg0 + kDec4Lead) / U), last = static_cast<int>((seg0 + V - 1) / U);
     const long long seg = static_cast<long long>(b) * p.Hkv + kvh;
     float M = -INFINITY;
     for (int i = first; i <= last; ++i) M = fmaxf(M, p.ws_ml[((i + seg) * g + hh) * 2]);
