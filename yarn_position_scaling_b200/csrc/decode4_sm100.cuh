@@ -20,7 +20,8 @@ constexpr int kDec4MaxBlocks = 640;  // most blocks of the split launch
 constexpr int kDec4Warps = 4;
 constexpr int kDec4Threads = kDec4Warps * 32;
 constexpr int kDec4Tile = 32;  // keys of one bulk copy
-constexpr int kDec4Stages = 3;
+constexpr int kDec4Stages = 2;
+constexpr int kDec4Step = 32;  // keys that a warp takes through scores and outputs at a time
 
 struct Decode4Params {
     const __nv_bfloat16 *q_new;          // [B][Hq][d]
@@ -127,11 +128,11 @@ __device__ __forceinline__ void mma0_f16_16816(float (&c)[4], uint32_t a0, uint3
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ void mma0_f16_1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+__device__ __forceinline__ void mma_f16_1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-        "{%7,%7,%7,%7};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -177,6 +178,7 @@ struct Decode4Smem {
     uint4 q_hi[8 * NT][HD / 8], q_lo[8 * NT][HD / 8];  // fragments, see the rotation below
     float q_sum[8 * NT][HD / kKv4Group];  // sums of the scaled query over the groups
     float q_scale[8 * NT];  // what takes the scaled query back
+    float slope[8 * NT];
     float m[kDec4Warps][8 * NT], l[kDec4Warps][8 * NT];
     uint64_t full[kDec4Warps][kDec4Stages];
     int abort;
@@ -195,20 +197,33 @@ constexpr size_t decode4_smem_bytes() {
 //   and exact.  The query is split into two fp16 parts.  Each 32-element group has its own
 //   accumulator, multiplied by the row's s in fp32; z (sum of q over the group) is one more
 //   product of fp16 operands, again with the sum in two parts.
+//   Up to four heads leave columns free: with REP = 2 (or 4, up to two heads) each head has
+//   REP of the eight.  Every second of them takes the query's second part, whose scores are
+//   then added across lanes, and each stands for its own groups in the value product, which
+//   divides the work on p s among the lanes that would else idle.
 //   Outputs: O^T[16 dims x 8 heads], value codes as A in the same way, B = p s in fp16; sum
 //   p z in fp32.  p = 2^(score - R) for a reference R per head that puts the largest p s of
-//   a tile at 2^12 and is raised only once one passes 2^15: small scales keep their bits
+//   a tile at 2^8 and is raised only once one passes 2^15: small scales keep their bits
 //   (fp16 holds 2^-14 at full precision), and the common tile costs one vote.
-template <int HD, int NT, bool kHalf>
-__global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
+template <int HD, int NT, int REP, bool kHalf>
+__global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     decode4_split_kernel(const __grid_constant__ Decode4Params p) {
     using Smem = Decode4Smem<HD, NT>;
     constexpr int kRow = kv4_row_bytes(HD), G = HD / kKv4Group;
+    static_assert(REP == 1 || (NT == 1 && REP <= G), "columns to spare");
+    constexpr int H = kDec4Step / 16;
+    constexpr int GL = G / REP;       // groups of a lane in the value product: k REP + copy
+    constexpr int kCopy = 4 / REP;    // lanes r of a copy; the next copy is as far away
     extern __shared__ uint8_t smem_raw[];
     Smem *sm = reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                         ~static_cast<uintptr_t>(127));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane >> 2, r = lane & 3;
-    const int g = p.group;
+    const int g = p.group, copy = r / kCopy;
+    // Where this lane's operands begin in a tile: row of fragment row c, and value codes of the
+    // rows of k indices 2r and 2r + 1.
+    const int key_at = dec4_key<HD>(c) * kRow;
+    const int val_at0 = dec4_key<HD>(2 * r) * kRow + HD / 2 + (G == 4 ? 8 : 4) * c;
+    const int val_at1 = dec4_key<HD>(2 * r + 1) * kRow + HD / 2 + (G == 4 ? 8 : 4) * c;
     const long long total = dec4_total(p, lane);
     const long long U = dec4_units_per_block(p, total);
     const long long u_lo = static_cast<long long>(blockIdx.x) * U;
@@ -224,9 +239,10 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
         fence_mbar_init();
     }
     __syncthreads();
-    uint32_t n_loads = 0, n_waits = 0;  // of this warp's ring, over all segments
+    // This warp's ring, over all segments: the stages of the next copy and the next wait,
+    // and the parity of the latter.
+    uint32_t s_load = 0, s_wait = 0, parity = 0;
     const uint64_t policy = l2_policy_evict_first();
-    bool ok = true;
 
     // Sequences before the first one of this block.
     int b = 0;
@@ -250,25 +266,42 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
             const int lo2 = rg.lo2 + max(u0, rg.len1) - rg.len1;
             const int hi2 = rg.lo2 + max(u1, rg.len1) - rg.len1;
             const int n_t1 = (hi1 - lo1 + kDec4Tile - 1) / kDec4Tile;
-            const int n_tiles = n_t1 + (hi2 - lo2 + kDec4Tile - 1) / kDec4Tile;
-            const bool has_L = u1 == rg.len1 + rg.len2;  // the new row is the last of this block's keys
+            // The new row is the last of the last block's keys: of the range that ends there.
+            const bool has_L = u1 == rg.len1 + rg.len2;
             uint8_t *plane = p.kv4 + (static_cast<long long>(b) * p.Hkv + kvh) * p.T_max * kRow;
-            auto tile_lo = [&](int i) { return i < n_t1 ? lo1 + i * kDec4Tile : lo2 + (i - n_t1) * kDec4Tile; };
-            auto tile_n = [&](int i) { return min(kDec4Tile, (i < n_t1 ? hi1 : hi2) - tile_lo(i)); };
-            auto load = [&](int i) {  // the cached rows of tile i: all but the new one
-                const int s = n_loads % kDec4Stages;
-                const int n = tile_n(i) - (has_L && i == n_tiles - 1 ? 1 : 0);
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sm->full[warp][s], n * kRow);
-                    if (n > 0)
-                        bulk_load(smem_u32(sm->ring[warp][s]), plane + static_cast<long long>(tile_lo(i)) * kRow,
-                                  n * kRow, &sm->full[warp][s], policy);
+            // This warp's tiles, as copies and as steps pass through them: every fourth of the
+            // first range, then of the second, the warps taking turns across the seam.
+            constexpr int kStride = kDec4Warps * kDec4Tile;
+            const int lo2w = lo2 + kDec4Tile * ((warp - n_t1) & (kDec4Warps - 1));
+            int ld_key = lo1 + kDec4Tile * warp, ld_end = hi1;
+            if (ld_key >= ld_end) {
+                ld_key = lo2w;
+                ld_end = hi2;
+            }
+            int key = ld_key, end = ld_end;
+            auto advance = [&](int &k, int &e) {
+                k += kStride;
+                if (k >= e && k < kStride + hi1 && e == hi1 && hi2 > lo2) {
+                    k = lo2w;
+                    e = hi2;
                 }
-                ++n_loads;
+            };
+            auto load = [&] {  // the cached rows of the next tile: all but the new one
+                if (lane == 0) {
+                    const int n = min(kDec4Tile, ld_end - ld_key);
+                    const uint32_t bytes = (n - (ld_key + n > L ? 1 : 0)) * kRow;
+                    uint64_t *bar = &sm->full[warp][s_load];
+                    mbar_arrive_expect_tx(bar, bytes);
+                    if (bytes > 0)
+                        bulk_load(smem_u32(sm->ring[warp][s_load]),
+                                  plane + static_cast<long long>(ld_key) * kRow, bytes, bar, policy);
+                }
+                s_load = s_load + 1 == kDec4Stages ? 0 : s_load + 1;
+                advance(ld_key, ld_end);
             };
 #pragma unroll
             for (int s = 0; s < kDec4Stages; ++s)
-                if (warp + s * kDec4Warps < n_tiles) load(warp + s * kDec4Warps);
+                if (ld_key < ld_end) load();
 
             // ---- queries: rotated, scaled, as fragments of two fp16 parts
             for (int i = tid; i < HD / 2; i += kDec4Threads) sm->cs[i] = kv4_cos_sin(L, p.turns[i]);
@@ -308,10 +341,17 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                 sm->q_hi[h][ch] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 sm->q_lo[h][ch] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 if ((ch & 3) == 0) sm->q_sum[h][ch >> 2] = sum;
-                if (ch == 0) sm->q_scale[h] = pow2i(e2 - 7);
+                if (ch == 0) {
+                    sm->q_scale[h] = pow2i(e2 - 7);
+                    // ALiBi's slope in units of a score before its scaling by sl2 q_scale.
+                    sm->slope[h] = p.alibi ? exp2f(-8.0f * static_cast<float>(kvh * g + h + 1) /
+                                                   static_cast<float>(p.Hq)) * 1.4426950408889634f /
+                                                 (p.sl2 * pow2i(e2 - 7))
+                                           : 0.f;
+                }
             }
-            const int last_warp = (n_tiles - 1) % kDec4Warps;
-            if (has_L && warp == last_warp) {
+            const int tile_L = hi2 > lo2 ? n_t1 + (L - lo2) / kDec4Tile : (L - lo1) / kDec4Tile;
+            if (has_L && warp == (tile_L & (kDec4Warps - 1))) {
                 dec4_append<HD, kHalf>(p, b, kvh, sm->new_row, sm->cs, lane);
                 __syncwarp();
                 if (lane < kRow / 16)
@@ -319,43 +359,34 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                         reinterpret_cast<const uint4 *>(sm->new_row)[lane];
             }
             __syncthreads();
-            uint32_t qh[2 * G][NT][2], ql[2 * G][NT][2], qz[NT];
-            float x_scale[NT][2], slope[NT][2];
+            // Of the two parts, this column's with copies, else both (from shared memory, in
+            // the loop: registers are short).
+            uint4 q_reg[G];
+            uint32_t qz[NT];
+            float x_scale[NT][2];
+            const int col_head = REP == 1 ? c : c % (8 / REP);
+            const bool second = REP > 1 && (c / (8 / REP)) % 2 == 1;
+            if constexpr (REP > 1) {
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+                    q_reg[gr] = second ? sm->q_lo[col_head][4 * gr + r] : sm->q_hi[col_head][4 * gr + r];
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int h = nt * 8 + c;
-#pragma unroll
-                for (int gr = 0; gr < G; ++gr) {
-                    const uint4 hi = sm->q_hi[h][4 * gr + r], lo = sm->q_lo[h][4 * gr + r];
-                    qh[2 * gr][nt][0] = hi.x;
-                    qh[2 * gr][nt][1] = hi.y;
-                    qh[2 * gr + 1][nt][0] = hi.z;
-                    qh[2 * gr + 1][nt][1] = hi.w;
-                    ql[2 * gr][nt][0] = lo.x;
-                    ql[2 * gr][nt][1] = lo.y;
-                    ql[2 * gr + 1][nt][0] = lo.z;
-                    ql[2 * gr + 1][nt][1] = lo.w;
-                }
+                const int h = nt * 8 + col_head;
                 // The z product: k = 2r, 2r+1 stand for the sums' first parts of the groups
                 // 2r, 2r+1 (r < 2) and for their second parts (r >= 2).
                 const int g0 = 2 * (r & 1);
-                const float z0 = g0 < G ? sm->q_sum[h][g0] : 0.f, z1 = g0 < G ? sm->q_sum[h][g0 + 1] : 0.f;
+                const float z0 = g0 < G && !second ? sm->q_sum[h][g0] : 0.f;
+                const float z1 = g0 < G && !second ? sm->q_sum[h][g0 + 1] : 0.f;
                 const __half2 hv = __floats2half2_rn(z0, z1);
                 qz[nt] = r < 2 ? *reinterpret_cast<const uint32_t *>(&hv)
                                : pack_half2(z0 - __low2float(hv), z1 - __high2float(hv));
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int col = nt * 8 + 2 * r + j;
-                    x_scale[nt][j] = p.sl2 * sm->q_scale[col];
-                    // The bias m (L - n) in units of x, before x_scale.
-                    slope[nt][j] = p.alibi ? exp2f(-8.0f * static_cast<float>(kvh * g + col + 1) /
-                                                   static_cast<float>(p.Hq)) * 1.4426950408889634f /
-                                                 x_scale[nt][j]
-                                           : 0.f;
-                }
+                for (int j = 0; j < 2; ++j) x_scale[nt][j] = p.sl2 * sm->q_scale[nt * 8 + 2 * (r % kCopy) + j];
             }
 
-            float o[G][2][NT][4], w[NT][2][G], l[NT][2], R[NT][2];
+            float o[G][2][NT][4], w[NT][2][GL], l[NT][2], R[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -363,217 +394,275 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                     R[nt][j] = -INFINITY;
                     l[nt][j] = 0.f;
 #pragma unroll
+                    for (int k = 0; k < GL; ++k) w[nt][j][k] = 0.f;
+#pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
-                        w[nt][j][gr] = 0.f;
                         o[gr][0][nt][j] = o[gr][0][nt][j + 2] = 0.f;
                         o[gr][1][nt][j] = o[gr][1][nt][j + 2] = 0.f;
                     }
                 }
 
-            for (int i = warp; i < n_tiles; i += kDec4Warps) {
-                const int s = n_waits % kDec4Stages;
-                ok = ok && mbar_wait_drain(&sm->full[warp][s], (n_waits / kDec4Stages) & 1, p.timeout_ns);
-                ++n_waits;
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
+            while (key < end) {
+                bool landed = mbar_try_wait(&sm->full[warp][s_wait], parity);
+                if (!__all_sync(0xffffffffu, landed)) {
+                    landed = mbar_wait_drain(&sm->full[warp][s_wait], parity, p.timeout_ns);
+                    if (!__all_sync(0xffffffffu, landed)) {
+                        // Give up: after the copies that are still under way, or their limit.
+                        if (lane == 0) raise_status(kStatusTimeoutDecode);
+                        sm->abort = 1;
+                        for (int k = 0; k < kDec4Stages && key < end; ++k) {
+                            mbar_wait_drain(&sm->full[warp][s_wait], parity, p.timeout_ns);
+                            if (++s_wait == kDec4Stages) {
+                                s_wait = 0;
+                                parity ^= 1;
+                            }
+                            advance(key, end);
+                        }
+                        break;
+                    }
                 }
-                uint8_t *ring = sm->ring[warp][s];
-                const int n0 = tile_lo(i), n_keys = tile_n(i);
-                if (has_L && i == n_tiles - 1) {
+                const uint8_t *ring = sm->ring[warp][s_wait];
+                if (++s_wait == kDec4Stages) {
+                    s_wait = 0;
+                    parity ^= 1;
+                }
+                const int n_keys = min(kDec4Tile, end - key);
+                if (key + n_keys > L) {  // the tile of the new row
                     if (lane < kRow / 16)
-                        reinterpret_cast<uint4 *>(ring + (n_keys - 1) * kRow)[lane] =
+                        reinterpret_cast<uint4 *>(const_cast<uint8_t *>(ring) + (n_keys - 1) * kRow)[lane] =
                             reinterpret_cast<const uint4 *>(sm->new_row)[lane];
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int sub = 0; sub < kDec4Tile; sub += 16) {
-                    if (sub >= n_keys) break;
-                    const int ka = sub + dec4_key<HD>(c), kb = ka + 8;  // this lane's keys
-                    const uint8_t *ra = ring + ka * kRow, *rb = ring + kb * kRow;
-                    uint32_t ca[G], cb[G], pa[G], pb[G];  // codes and (s, z) of the two keys
-                    if constexpr (G == 4) {
-                        *reinterpret_cast<uint4 *>(ca) = *reinterpret_cast<const uint4 *>(ra + 16 * r);
-                        *reinterpret_cast<uint4 *>(cb) = *reinterpret_cast<const uint4 *>(rb + 16 * r);
-                        *reinterpret_cast<uint4 *>(pa) = *reinterpret_cast<const uint4 *>(ra + HD);
-                        *reinterpret_cast<uint4 *>(pb) = *reinterpret_cast<const uint4 *>(rb + HD);
-                    } else {
-                        *reinterpret_cast<uint2 *>(ca) = *reinterpret_cast<const uint2 *>(ra + 8 * r);
-                        *reinterpret_cast<uint2 *>(cb) = *reinterpret_cast<const uint2 *>(rb + 8 * r);
-                        *reinterpret_cast<uint2 *>(pa) = *reinterpret_cast<const uint2 *>(ra + HD);
-                        *reinterpret_cast<uint2 *>(pb) = *reinterpret_cast<const uint2 *>(rb + HD);
-                    }
-                    float x[NT][4], xz[NT][4];
-                    {
-                        const int at = HD + (G == 4 ? 8 * (r & 1) : 0);
-                        const uint2 wa = *reinterpret_cast<const uint2 *>(ra + at);
-                        const uint2 wb = *reinterpret_cast<const uint2 *>(rb + at);
-                        const uint32_t za = __byte_perm(wa.x, wa.y, 0x7632), zb = __byte_perm(wb.x, wb.y, 0x7632);
+                for (int k0 = 0; k0 < n_keys; k0 += 16 * H) {
+                // The lane's keys are fragment rows c and c + 8 of each of the step's 16 keys.
+                const uint8_t *row0 = ring + key_at + k0 * kRow;
+                // ---- scores over x_scale
+                float x[H][NT][4];
+                {
+                    uint32_t code[H][2][G];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma0_f16_1688(xz[nt], za, zb, qz[nt]);
-                    }
+                    for (int t = 0; t < H; ++t)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint8_t *from = row0 + (16 * t + 8 * k) * kRow + 4 * G * r;
+                            if constexpr (G == 4)
+                                *reinterpret_cast<uint4 *>(code[t][k]) = *reinterpret_cast<const uint4 *>(from);
+                            else
+                                *reinterpret_cast<uint2 *>(code[t][k]) = *reinterpret_cast<const uint2 *>(from);
+                        }
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
-                        float acc[NT][4];
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            const uint32_t wa = ca[gr] >> (8 * part), wb = cb[gr] >> (8 * part);
-                            const uint32_t a0 = wa & 0x000f000fu, a2 = wa & 0x00f000f0u;
-                            const uint32_t a1 = wb & 0x000f000fu, a3 = wb & 0x00f000f0u;
+                        uint4 hi[NT], lo[NT];
+                        if constexpr (REP > 1) {
+                            hi[0] = q_reg[gr];
+                        } else {
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                if (part == 0)
-                                    mma0_f16_16816(acc[nt], a0, a1, a2, a3, qh[2 * gr][nt][0], qh[2 * gr][nt][1]);
-                                else
-                                    mma_f16_16816(acc[nt], a0, a1, a2, a3, qh[2 * gr + 1][nt][0], qh[2 * gr + 1][nt][1]);
-                                mma_f16_16816(acc[nt], a0, a1, a2, a3, ql[2 * gr + part][nt][0], ql[2 * gr + part][nt][1]);
+                                hi[nt] = sm->q_hi[nt * 8 + c][4 * gr + r];
+                                lo[nt] = sm->q_lo[nt * 8 + c][4 * gr + r];
                             }
                         }
-                        const float sa = lo_f(pa[gr]), sb = lo_f(pb[gr]);
+#pragma unroll
+                        for (int t = 0; t < H; ++t) {
+                            const uint32_t wa = code[t][0][gr], wb = code[t][1][gr];
+                            const uint32_t va = wa >> 8, vb = wb >> 8;
+                            const uint8_t *from = row0 + 16 * t * kRow + HD + 4 * gr;
+                            const float sa = __half2float(*reinterpret_cast<const __half *>(from));
+                            const float sb = __half2float(*reinterpret_cast<const __half *>(from + 8 * kRow));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float acc[4];
+                                mma0_f16_16816(acc, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, hi[nt].x, hi[nt].y);
+                                mma_f16_16816(acc, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, hi[nt].z, hi[nt].w);
+                                if constexpr (REP == 1) {
+                                    mma_f16_16816(acc, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, lo[nt].x, lo[nt].y);
+                                    mma_f16_16816(acc, va & 0x000f000fu, vb & 0x000f000fu, va & 0x00f000f0u, vb & 0x00f000f0u, lo[nt].z, lo[nt].w);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    x[t][nt][e] = gr == 0 ? (e < 2 ? sa : sb) * acc[e] : fmaf(e < 2 ? sa : sb, acc[e], x[t][nt][e]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < H; ++t) {
+                        const uint8_t *from = row0 + 16 * t * kRow + HD + (G == 4 ? 8 * (r & 1) : 0);
+                        const uint2 za = *reinterpret_cast<const uint2 *>(from);
+                        const uint2 zb = *reinterpret_cast<const uint2 *>(from + 8 * kRow);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                x[nt][e] = gr == 0 ? (e < 2 ? sa : sb) * acc[nt][e]
-                                                   : fmaf(e < 2 ? sa : sb, acc[nt][e], x[nt][e]);
-                        }
-                    }
-                    // ---- scores over x_scale; then the values' (s, z) of the two keys
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(x[nt][e], 16777216.f, xz[nt][e]);
-                    if constexpr (G == 4) {
-                        *reinterpret_cast<uint4 *>(pa) = *reinterpret_cast<const uint4 *>(ra + HD + 4 * G);
-                        *reinterpret_cast<uint4 *>(pb) = *reinterpret_cast<const uint4 *>(rb + HD + 4 * G);
-                    } else {
-                        *reinterpret_cast<uint2 *>(pa) = *reinterpret_cast<const uint2 *>(ra + HD + 4 * G);
-                        *reinterpret_cast<uint2 *>(pb) = *reinterpret_cast<const uint2 *>(rb + HD + 4 * G);
-                    }
-                    if (p.alibi) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                            for (int e = 0; e < 4; ++e) x[t][nt][e] *= 16777216.f;
+                            mma_f16_1688(x[t][nt], __byte_perm(za.x, za.y, 0x7632), __byte_perm(zb.x, zb.y, 0x7632), qz[nt]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                x[nt][e] = fmaf(-slope[nt][e & 1], static_cast<float>(L - n0 - (e < 2 ? ka : kb)), x[nt][e]);
-                    }
-                    if (n_keys < kDec4Tile) {  // rows behind the tile's end do not count
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if ((e < 2 ? ka : kb) >= n_keys) x[nt][e] = -INFINITY;
-#pragma unroll
-                        for (int gr = 0; gr < G; ++gr) {
-                            if (ka >= n_keys) pa[gr] = 0;
-                            if (kb >= n_keys) pb[gr] = 0;
+                                if constexpr (REP > 1) x[t][nt][e] += __shfl_xor_sync(0xffffffffu, x[t][nt][e], kCopy);
                         }
                     }
-                    float pr[NT][4];
-                    uint32_t bf[G][NT][2];
-                    // Probabilities and B operands; true if one of the latter nears fp16's end
-                    // (or would, but for a scale of 0).
-                    auto products = [&] {
+                }
+                uint32_t par[H][2][GL];  // the values' (s, z) of this lane's groups
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                for (int t = 0; t < H; ++t)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) pr[nt][e] = ex2f(fmaf(x[nt][e], x_scale[nt][e & 1], -R[nt][e & 1]));
-                        float p_max = 0.f;
-                        __half2 t = __half2half2(__ushort_as_half(0));
+                    for (int k = 0; k < 2; ++k) {
+                        const uint8_t *from = row0 + (16 * t + 8 * k) * kRow + HD + 4 * G;
+                        if constexpr (GL == 4) {
+                            *reinterpret_cast<uint4 *>(par[t][k]) = *reinterpret_cast<const uint4 *>(from);
+                        } else {
 #pragma unroll
-                        for (int gr = 0; gr < G; ++gr) {
-                            const float sa = lo_f(pa[gr]), sb = lo_f(pb[gr]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                bf[gr][nt][0] = pack_half2(pr[nt][0] * sa, pr[nt][1] * sa);
-                                bf[gr][nt][1] = pack_half2(pr[nt][2] * sb, pr[nt][3] * sb);
-                                t = __hmax2(t, *reinterpret_cast<const __half2 *>(&bf[gr][nt][0]));
-                                t = __hmax2(t, *reinterpret_cast<const __half2 *>(&bf[gr][nt][1]));
-                            }
+                            for (int i = 0; i < GL; ++i)
+                                par[t][k][i] = reinterpret_cast<const uint32_t *>(from)[i * REP + copy];
                         }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            p_max = fmaxf(p_max, fmaxf(fmaxf(pr[nt][0], pr[nt][1]), fmaxf(pr[nt][2], pr[nt][3])));
-                        const uint32_t largest = *reinterpret_cast<const uint32_t *>(&t);
-                        return ((largest + 0x08000800u) & 0x80008000u) != 0 || p_max > 1.1e12f;
-                    };
-                    if (__any_sync(0xffffffffu, products())) {
-                        // Raise the references to these keys' largest p s, put at 2^12 (a scale
-                        // below fp16's smallest counts as that).
-                        float sa = 0.f, sb = 0.f;
-#pragma unroll
-                        for (int gr = 0; gr < G; ++gr) {
-                            sa = fmaxf(sa, lo_f(pa[gr]));
-                            sb = fmaxf(sb, lo_f(pb[gr]));
-                        }
-                        sa = log2f(fmaxf(sa, 5.9604645e-8f)) - 12.f;
-                        sb = log2f(fmaxf(sb, 5.9604645e-8f)) - 12.f;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                float t = fmaxf(fmaf(x[nt][j], x_scale[nt][j], sa), fmaf(x[nt][j + 2], x_scale[nt][j], sb));
-#pragma unroll
-                                for (int off = 4; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-                                t = fmaxf(t, R[nt][j]);
-                                if (!(fabsf(t) < INFINITY)) t = R[nt][j] == -INFINITY ? 0.f : R[nt][j];
-                                const float f = R[nt][j] == -INFINITY ? 0.f : ex2f(R[nt][j] - t);
-                                R[nt][j] = t;
-                                l[nt][j] *= f;
-#pragma unroll
-                                for (int gr = 0; gr < G; ++gr) {
-                                    w[nt][j][gr] *= f;
-                                    o[gr][0][nt][j] *= f;
-                                    o[gr][0][nt][j + 2] *= f;
-                                    o[gr][1][nt][j] *= f;
-                                    o[gr][1][nt][j + 2] *= f;
-                                }
-                            }
-                        products();
                     }
-                    // ---- sums, and O^T += V^T P
+                if (p.alibi) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            l[nt][j] += pr[nt][j] + pr[nt][j + 2];
+                            const float slope = sm->slope[nt * 8 + 2 * (r % kCopy) + j];
 #pragma unroll
-                            for (int gr = 0; gr < G; ++gr)
-                                w[nt][j][gr] = fmaf(pr[nt][j], hi_f(pa[gr]), fmaf(pr[nt][j + 2], hi_f(pb[gr]), w[nt][j][gr]));
+                            for (int t = 0; t < H; ++t)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    x[t][nt][2 * k + j] = fmaf(-slope, static_cast<float>(L - key - (k0 + 16 * t + 8 * k + dec4_key<HD>(c))), x[t][nt][2 * k + j]);
+                        }
+                }
+                if (n_keys < kDec4Tile) {  // rows behind the tile's end do not count
+#pragma unroll
+                    for (int t = 0; t < H; ++t)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (k0 + 16 * t + 8 * k + dec4_key<HD>(c) >= n_keys) {
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) x[t][nt][2 * k] = x[t][nt][2 * k + 1] = -INFINITY;
+#pragma unroll
+                                for (int i = 0; i < GL; ++i) par[t][k][i] = 0;
+                            }
+                }
+                // Probabilities and B operands; true if one of the latter nears fp16's end (or
+                // would, but for a scale of 0).
+                float pr[H][NT][4];
+                uint32_t bf[H][GL][NT][2];
+                auto products = [&] {
+                    float p_max[H * NT];
+                    __half2 top[H * NT * GL];
+#pragma unroll
+                    for (int t = 0; t < H; ++t)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                pr[t][nt][e] = ex2f(fmaf(x[t][nt][e], x_scale[nt][e & 1], -R[nt][e & 1]));
+                            }
+                            p_max[t * NT + nt] = fmaxf(fmaxf(pr[t][nt][0], pr[t][nt][1]), fmaxf(pr[t][nt][2], pr[t][nt][3]));
+#pragma unroll
+                            for (int i = 0; i < GL; ++i) {
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const float s = lo_f(par[t][k][i]);
+                                    bf[t][i][nt][k] = pack_half2(pr[t][nt][2 * k] * s, pr[t][nt][2 * k + 1] * s);
+                                }
+                                top[(t * NT + nt) * GL + i] = __hmax2(*reinterpret_cast<const __half2 *>(&bf[t][i][nt][0]),
+                                                                      *reinterpret_cast<const __half2 *>(&bf[t][i][nt][1]));
+                            }
+                        }
+#pragma unroll
+                    for (int n = H * NT * GL / 2; n > 0; n >>= 1)
+#pragma unroll
+                        for (int i = 0; i < n; ++i) top[i] = __hmax2(top[i], top[i + n]);
+#pragma unroll
+                    for (int n = H * NT / 2; n > 0; n >>= 1)
+#pragma unroll
+                        for (int i = 0; i < n; ++i) p_max[i] = fmaxf(p_max[i], p_max[i + n]);
+                    const uint32_t largest = *reinterpret_cast<const uint32_t *>(&top[0]);
+                    return ((largest + 0x08000800u) & 0x80008000u) != 0 || p_max[0] > 1.1e12f;  // 2^15; 2^40
+                };
+                if (__any_sync(0xffffffffu, products())) {
+                    // Raise the references to these keys' largest p s, put at 2^8 (a scale below
+                    // fp16's smallest counts as that).
+                    float ls[H][2];
+#pragma unroll
+                    for (int t = 0; t < H; ++t)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float s = 5.9604645e-8f;
+#pragma unroll
+                            for (int i = 0; i < GL; ++i) s = fmaxf(s, lo_f(par[t][k][i]));
+                            ls[t][k] = log2f(s) - 8.f;
+                        }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float t = R[nt][j];
+#pragma unroll
+                            for (int k = 0; k < 2 * H; ++k)
+                                t = fmaxf(t, fmaf(x[k >> 1][nt][2 * (k & 1) + j], x_scale[nt][j], ls[k >> 1][k & 1]));
+#pragma unroll
+                            for (int off = kCopy; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+                            if (!(fabsf(t) < INFINITY)) t = R[nt][j] == -INFINITY ? 0.f : R[nt][j];
+                            const float f = R[nt][j] == -INFINITY ? 0.f : ex2f(R[nt][j] - t);
+                            R[nt][j] = t;
+                            l[nt][j] *= f;
+#pragma unroll
+                            for (int i = 0; i < GL; ++i) w[nt][j][i] *= f;
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr) {
+                                o[gr][0][nt][j] *= f;
+                                o[gr][0][nt][j + 2] *= f;
+                                o[gr][1][nt][j] *= f;
+                                o[gr][1][nt][j + 2] *= f;
+                            }
+                        }
+                    products();
+                }
+                // ---- sums, and O^T += V^T P
+#pragma unroll
+                for (int t = 0; t < H; ++t) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            l[nt][j] += pr[t][nt][j] + pr[t][nt][j + 2];
+#pragma unroll
+                            for (int i = 0; i < GL; ++i)
+                                w[nt][j][i] = fmaf(pr[t][nt][j], hi_f(par[t][0][i]), fmaf(pr[t][nt][j + 2], hi_f(par[t][1][i]), w[nt][j][i]));
                         }
                     uint32_t vw[4][G / 2];  // value words of the four keys of this lane's k indices
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint8_t *row = ring + (sub + dec4_key<HD>((k >> 1) * 8 + 2 * r + (k & 1))) * kRow + HD / 2;
+                        const uint8_t *from = ring + (k & 1 ? val_at1 : val_at0) + (k0 + 16 * t + 8 * (k >> 1)) * kRow;
                         if constexpr (G == 4)
-                            *reinterpret_cast<uint2 *>(vw[k]) = *reinterpret_cast<const uint2 *>(row + 8 * c);
+                            *reinterpret_cast<uint2 *>(vw[k]) = *reinterpret_cast<const uint2 *>(from);
                         else
-                            vw[k][0] = *reinterpret_cast<const uint32_t *>(row + 4 * c);
+                            vw[k][0] = *reinterpret_cast<const uint32_t *>(from);
                     }
+                    uint32_t b0[GL][NT], b1[GL][NT];
+#pragma unroll
+                    for (int i = 0; i < GL; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            b0[i][nt] = transpose8(bf[t][i][nt][0]);
+                            b1[i][nt] = transpose8(bf[t][i][nt][1]);
+                        }
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
                         const uint32_t sel = gr & 1 ? 0x7632u : 0x5410u;
                         const uint32_t u = __byte_perm(vw[0][gr / 2], vw[1][gr / 2], sel);
-                        const uint32_t t = __byte_perm(vw[2][gr / 2], vw[3][gr / 2], sel);
-                        uint32_t b0[NT], b1[NT];
+                        const uint32_t v = __byte_perm(vw[2][gr / 2], vw[3][gr / 2], sel);
+                        const uint32_t us = u >> 8, vs = v >> 8;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            b0[nt] = transpose8(bf[gr][nt][0]);
-                            b1[nt] = transpose8(bf[gr][nt][1]);
-                        }
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const uint32_t us = u >> (8 * m), ts = t >> (8 * m);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma_f16_16816(o[gr][m][nt], us & 0x000f000fu, us & 0x00f000f0u,
-                                              ts & 0x000f000fu, ts & 0x00f000f0u, b0[nt], b1[nt]);
+                            mma_f16_16816(o[gr][0][nt], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0[gr / REP][nt], b1[gr / REP][nt]);
+                            mma_f16_16816(o[gr][1][nt], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, b0[gr / REP][nt], b1[gr / REP][nt]);
                         }
                     }
                 }
+                }
                 __syncwarp();  // the whole warp is done with the stage
-                const int nxt = i + kDec4Stages * kDec4Warps;
-                if (nxt < n_tiles) load(nxt);
+                advance(key, end);
+                if (ld_key < ld_end) load();
             }
 
             // ---- the warps' results: outputs of head h, dims, in place of the ring
@@ -585,36 +674,30 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : HD == 128 ? 3 : 4)
                     for (int off = 4; off < 32; off <<= 1) {
                         l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
 #pragma unroll
-                        for (int gr = 0; gr < G; ++gr)
-                            w[nt][j][gr] += __shfl_xor_sync(0xffffffffu, w[nt][j][gr], off);
+                        for (int i = 0; i < GL; ++i)
+                            w[nt][j][i] += __shfl_xor_sync(0xffffffffu, w[nt][j][i], off);
                     }
-                    if (lane < 4) {
+                    if (lane < kCopy) {
                         sm->m[warp][nt * 8 + 2 * r + j] = R[nt][j];
                         sm->l[warp][nt * 8 + 2 * r + j] = l[nt][j];
                     }
                 }
-            if (!ok) {  // a copy did not land: no partial result to trust
-                raise_status(kStatusTimeoutDecode);
-                sm->abort = 1;
-                for (; n_waits < n_loads; ++n_waits)  // the copies still under way
-                    mbar_wait_drain(&sm->full[warp][n_waits % kDec4Stages],
-                                    (n_waits / kDec4Stages) & 1, p.timeout_ns);
-            }
             __syncthreads();
-            if (sm->abort) return;
+            if (sm->abort) return;  // a copy did not land: no partial result to trust
             float *red = reinterpret_cast<float *>(&sm->ring[0][0][0]);  // [warps][8 NT][HD]
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
+                if (gr % REP != copy) continue;  // another copy's group
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float add = w[nt][j][gr];
+                        const float add = w[nt][j][gr / REP];
                         const float4 out = make_float4(fmaf(o[gr][0][nt][j], 16777216.f, add),
                                                        fmaf(o[gr][0][nt][j + 2], 1048576.f, add),
                                                        fmaf(o[gr][1][nt][j], 16777216.f, add),
                                                        fmaf(o[gr][1][nt][j + 2], 1048576.f, add));
-                        *reinterpret_cast<float4 *>(red + (warp * 8 * NT + nt * 8 + 2 * r + j) * HD + 32 * gr + 4 * c) = out;
+                        *reinterpret_cast<float4 *>(red + (warp * 8 * NT + nt * 8 + 2 * (r % kCopy) + j) * HD + 32 * gr + 4 * c) = out;
                     }
             }
             __syncthreads();

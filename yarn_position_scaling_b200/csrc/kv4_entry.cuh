@@ -95,13 +95,13 @@ size_t decode4_ws_bytes(long long B, long long Hq, long long Hkv, long long d) {
 }
 
 // One wave of the split kernel, and the places of its partial results.
-template <int HD, int NT, bool kHalf>
-int launch_decode4(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
+template <int HD, int NT, int REP, bool kHalf>
+int launch_decode4_form(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
     static int per_sm = 0;  // same value on every device of this build's target
     if (per_sm == 0) {
         int n = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &n, yr::decode4_split_kernel<HD, NT, kHalf>, yr::kDec4Threads,
+                &n, yr::decode4_split_kernel<HD, NT, REP, kHalf>, yr::kDec4Threads,
                 yr::decode4_smem_bytes<HD, NT>()) != cudaSuccess ||
             n < 1)
             n = 1;
@@ -111,11 +111,21 @@ int launch_decode4(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
     dp.grid_blocks = blocks < yr::kDec4MaxBlocks ? blocks : yr::kDec4MaxBlocks;
     const long long slots = dp.grid_blocks + static_cast<long long>(dp.B) * dp.Hkv;
     dp.ws_ml = dp.ws_o + slots * dp.group * HD;
-    yr::decode4_split_kernel<HD, NT, kHalf>
+    yr::decode4_split_kernel<HD, NT, REP, kHalf>
         <<<dp.grid_blocks, yr::kDec4Threads, yr::decode4_smem_bytes<HD, NT>(), st>>>(dp);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("decode4_split_kernel launch", e);
     return YR_OK;
+}
+
+// The form of the kernel for g query heads per KV head.
+template <int HD, bool kHalf>
+int launch_decode4(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
+    const int g = dp.group;
+    if (g > 8) return launch_decode4_form<HD, 2, 1, kHalf>(dp, sm_count, st);
+    if (g > 4) return launch_decode4_form<HD, 1, 1, kHalf>(dp, sm_count, st);
+    if (g > 2 || HD == 64) return launch_decode4_form<HD, 1, 2, kHalf>(dp, sm_count, st);
+    return launch_decode4_form<HD, 1, HD / 32, kHalf>(dp, sm_count, st);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -248,16 +258,10 @@ extern "C" int yr_attn_decode_kv4(const void *q_new, const void *k_new, const vo
     dp.timeout_ns = wait_timeout_ns();
     dp.ws_o = static_cast<float *>(workspace);
     const bool half = tab->pairs == YR_PAIR_HALF;
-    if (d == 128)
-        rc = g <= 8 ? half ? launch_decode4<128, 1, true>(dp, sm_count, st)
-                           : launch_decode4<128, 1, false>(dp, sm_count, st)
-             : half ? launch_decode4<128, 2, true>(dp, sm_count, st)
-                    : launch_decode4<128, 2, false>(dp, sm_count, st);
-    else
-        rc = g <= 8 ? half ? launch_decode4<64, 1, true>(dp, sm_count, st)
-                           : launch_decode4<64, 1, false>(dp, sm_count, st)
-             : half ? launch_decode4<64, 2, true>(dp, sm_count, st)
-                    : launch_decode4<64, 2, false>(dp, sm_count, st);
+    rc = d == 128 ? half ? launch_decode4<128, true>(dp, sm_count, st)
+                         : launch_decode4<128, false>(dp, sm_count, st)
+         : half   ? launch_decode4<64, true>(dp, sm_count, st)
+                  : launch_decode4<64, false>(dp, sm_count, st);
     if (rc != YR_OK) return rc;
     const unsigned merge = static_cast<unsigned>(B) * Hq;
     if (d == 128)

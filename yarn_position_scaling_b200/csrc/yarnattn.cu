@@ -152,22 +152,15 @@ int prepare_device(int *sm_count, DeviceState *out = nullptr) {
                  yr::decode_smem_bytes<64>()},
                 {reinterpret_cast<const void *>(&yr::decode_split_kernel<64, 2>),
                  yr::decode_smem_bytes<64>()},
-                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<128, 1, false>),
-                 yr::decode4_smem_bytes<128, 1>()},
-                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<128, 1, true>),
-                 yr::decode4_smem_bytes<128, 1>()},
-                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<128, 2, false>),
-                 yr::decode4_smem_bytes<128, 2>()},
-                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<128, 2, true>),
-                 yr::decode4_smem_bytes<128, 2>()},
-                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<64, 1, false>),
-                 yr::decode4_smem_bytes<64, 1>()},
-                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<64, 1, true>),
-                 yr::decode4_smem_bytes<64, 1>()},
-                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<64, 2, false>),
-                 yr::decode4_smem_bytes<64, 2>()},
-                {reinterpret_cast<const void *>(&yr::decode4_split_kernel<64, 2, true>),
-                 yr::decode4_smem_bytes<64, 2>()},
+#define YR_DECODE4(HD, NT, REP)                                                        \
+    {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, false>),    \
+     yr::decode4_smem_bytes<HD, NT>()},                                                \
+        {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, true>), \
+         yr::decode4_smem_bytes<HD, NT>()}
+                YR_DECODE4(128, 1, 4), YR_DECODE4(128, 1, 2), YR_DECODE4(128, 1, 1),
+                YR_DECODE4(128, 2, 1), YR_DECODE4(64, 1, 2), YR_DECODE4(64, 1, 1),
+                YR_DECODE4(64, 2, 1),
+#undef YR_DECODE4
             };
             for (auto &a : attrs) {
                 e = cudaFuncSetAttribute(a.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
