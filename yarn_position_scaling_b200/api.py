@@ -468,36 +468,42 @@ def kv4_cache(B: int, Hkv: int, T_max: int, d: int, device="cuda") -> torch.Tens
     return torch.zeros((B, Hkv, T_max, n), dtype=torch.uint8, device=device)
 
 
-def _kv4_tensors(fn, kv4, tensors):
-    """Checks a 4-bit cache and the tensors (name, tensor, dtype, shape) used with it: all
-    contiguous on its device, except those whose shape is given as a list, which may be
-    strided.  None is an argument left out."""
-    dev = kv4.device
+# The calls below are made once per layer and token, so what they do in Python is kept short:
+# pointers go over as plain integers and the current stream's handle is asked for directly.
+def _kv4_cache_of(fn, kv4, B, Hkv, d):
+    """Checks the cache and returns its device."""
     if not kv4.is_cuda or kv4.dtype != torch.uint8 or kv4.dim() != 4 or not kv4.is_contiguous():
         raise ValueError(f"{fn}: kv4 must be a contiguous uint8 CUDA tensor [B, Hkv, T_max, 5d/4]")
-    for name, t, dtype, shape in tensors:
-        if t is None:
-            continue
-        if t.device != dev or t.dtype != dtype:
-            raise ValueError(f"{fn}: {name} must be a {dtype} tensor on {dev}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{fn}: {name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-        if not isinstance(shape, list) and not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be contiguous")
+    if kv4.shape[0] != B or kv4.shape[1] != Hkv or kv4.shape[3] * 4 != 5 * d:
+        raise ValueError(f"{fn}: kv4 must have the shape {(B, Hkv, 'T_max', 5 * d / 4)}, "
+                         f"not {tuple(kv4.shape)}")
+    return kv4.device
 
 
-def _kv4_call(dev, fn, args, stream):
-    """fn(*args, stream) with the tensors' device current, on its current stream if none is given."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
-    else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+def _kv4_arg(fn, name, t, dev, dtype, shape, strided=False):
+    """The address of tensor t after checking it (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{fn}: {name} must be a {dtype} tensor on {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} must have the shape {shape}, not {tuple(t.shape)}")
+    if not strided and not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _kv4_workspace(fn, ws, dev):
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous tensor on {dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _kv4_strides(fn, name, t):
-    """Strides over b, h and t.  Those of axes of one element are never used and may be
-    anything in torch; they are passed on as those of a contiguous tensor."""
+    """Strides over b, h and t, or None if contiguous.  Those of axes of one element are never
+    used and may be anything in torch; they are passed on as those of a contiguous tensor."""
+    if t.is_contiguous():
+        return None
     if t.stride(3) != 1:
         raise ValueError(f"{fn}: {name} must have unit stride over d")
     st, n = [], t.shape[3]
@@ -507,20 +513,33 @@ def _kv4_strides(fn, name, t):
     return (ctypes.c_int64 * 3)(*st)
 
 
+def _kv4_call(dev, fn, args, stream):
+    """fn(*args, stream) with the tensors' device current, on its current stream if none is given."""
+    if stream is not None:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index == torch._C._cuda_getDevice():
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, handle))
+
+
 def kv4_write(k, v, kv4, table: RopeTable, pos0: int = 0, starts=None, counts=None, stream=None):
     """Rotate, quantise and write k, v [B,Hkv,T,d] bf16 (any strides with unit stride over d)
     into the 4-bit cache: row t of sequence b goes to slot pos0 + starts[b] + t.  starts and
     counts are int32 [B] on the device (None: 0 and T); rows t >= counts[b] are left out.
     Returns kv4."""
     B, Hkv, T, d = k.shape
-    _kv4_tensors("kv4_write", kv4, [
-        ("kv4", kv4, torch.uint8, (B, Hkv, kv4.shape[2], 5 * d // 4)),
-        ("k", k, torch.bfloat16, [B, Hkv, T, d]), ("v", v, torch.bfloat16, [B, Hkv, T, d]),
-        ("starts", starts, torch.int32, (B,)), ("counts", counts, torch.int32, (B,))])
-    _kv4_call(kv4.device, load().yr_kv4_write,
-              (_ptr(k), _ptr(v), _ptr(kv4), B, Hkv, T, d, kv4.shape[2],
-               _kv4_strides("kv4_write", "k", k), _kv4_strides("kv4_write", "v", v), int(pos0),
-               _ptr(starts), _ptr(counts), ctypes.byref(table)), stream)
+    fn, shape = "kv4_write", (B, Hkv, T, d)
+    dev = _kv4_cache_of(fn, kv4, B, Hkv, d)
+    _kv4_call(dev, load().yr_kv4_write,
+              (_kv4_arg(fn, "k", k, dev, torch.bfloat16, shape, True),
+               _kv4_arg(fn, "v", v, dev, torch.bfloat16, shape, True), kv4.data_ptr(), B, Hkv, T,
+               d, kv4.shape[2], _kv4_strides(fn, "k", k), _kv4_strides(fn, "v", v), int(pos0),
+               _kv4_arg(fn, "starts", starts, dev, torch.int32, (B,)),
+               _kv4_arg(fn, "counts", counts, dev, torch.int32, (B,)), ctypes.byref(table)), stream)
     return kv4
 
 
@@ -531,27 +550,27 @@ def kv4_read(kv4, T: int, pos0: int = 0, starts=None, counts=None, dtype=torch.b
     (bf16 or fp16); outputs given as k and v are written in place (any strides with unit
     stride over d) and keep the rows that are not read, others are allocated, with zeros
     there."""
-    B, Hkv, T_max, n = kv4.shape
-    d = n * 4 // 5
+    fn = "kv4_read"
     if dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("kv4_read: dtype must be torch.bfloat16 or torch.float16")
-    zero_rest = k is None and v is None
+    B, Hkv, T_max, n = kv4.shape
+    d, T = n * 4 // 5, int(T)
+    dev = _kv4_cache_of(fn, kv4, B, Hkv, d)
+    shape, zero_rest = (B, Hkv, T, d), k is None and v is None
     if zero_rest:
-        k = torch.empty((B, Hkv, T, d), dtype=dtype, device=kv4.device)
-        v = torch.empty_like(k)
+        k = torch.empty(shape, dtype=dtype, device=dev)
+        v = torch.empty(shape, dtype=dtype, device=dev)
     elif k is None:
-        k = torch.zeros((B, Hkv, T, d), dtype=dtype, device=kv4.device)
+        k = torch.zeros(shape, dtype=dtype, device=dev)
     elif v is None:
-        v = torch.zeros((B, Hkv, T, d), dtype=dtype, device=kv4.device)
-    _kv4_tensors("kv4_read", kv4, [
-        ("kv4", kv4, torch.uint8, (B, Hkv, T_max, 5 * d // 4)),
-        ("k", k, dtype, [B, Hkv, T, d]), ("v", v, dtype, [B, Hkv, T, d]),
-        ("starts", starts, torch.int32, (B,)), ("counts", counts, torch.int32, (B,))])
-    _kv4_call(kv4.device, load().yr_kv4_read,
-              (_ptr(kv4), _ptr(k), _ptr(v), KV4_BF16 if dtype == torch.bfloat16 else KV4_FP16, B,
-               Hkv, T, d, T_max, _kv4_strides("kv4_read", "k", k),
-               _kv4_strides("kv4_read", "v", v), int(pos0), _ptr(starts), _ptr(counts),
-               int(zero_rest)), stream)
+        v = torch.zeros(shape, dtype=dtype, device=dev)
+    _kv4_call(dev, load().yr_kv4_read,
+              (kv4.data_ptr(), _kv4_arg(fn, "k", k, dev, dtype, shape, True),
+               _kv4_arg(fn, "v", v, dev, dtype, shape, True),
+               KV4_BF16 if dtype == torch.bfloat16 else KV4_FP16, B, Hkv, T, d, T_max,
+               _kv4_strides(fn, "k", k), _kv4_strides(fn, "v", v), int(pos0),
+               _kv4_arg(fn, "starts", starts, dev, torch.int32, (B,)),
+               _kv4_arg(fn, "counts", counts, dev, torch.int32, (B,)), int(zero_rest)), stream)
     return k, v
 
 
@@ -566,26 +585,26 @@ def attn_decode_kv4(q_new, k_new, v_new, kv4, cache_len, table: RopeTable, windo
     cache_len int32 [B] on the device.  Writes slot cache_len[b]; returns the output [B,Hq,d]
     bf16.  lse fp32 [B,Hq] and k_stored, v_stored bf16 [B,Hkv,d] (the new row as the cache
     holds it) are filled if given."""
+    fn, bf = "attn_decode_kv4", torch.bfloat16
     B, Hq, d = q_new.shape
     Hkv, T_max = kv4.shape[1], kv4.shape[2]
+    dev = _kv4_cache_of(fn, kv4, B, Hkv, d)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=kv4.device)
+        out = torch.empty((B, Hq, d), dtype=bf, device=dev)
     if workspace is None:
         workspace = torch.empty(attn_decode_kv4_workspace_bytes(B, Hq, Hkv, d),
-                                dtype=torch.uint8, device=kv4.device)
-    bf = torch.bfloat16
-    _kv4_tensors("attn_decode_kv4", kv4, [
-        ("kv4", kv4, torch.uint8, (B, Hkv, T_max, 5 * d // 4)), ("q_new", q_new, bf, (B, Hq, d)),
-        ("k_new", k_new, bf, (B, Hkv, d)), ("v_new", v_new, bf, (B, Hkv, d)),
-        ("cache_len", cache_len, torch.int32, (B,)), ("out", out, bf, (B, Hq, d)),
-        ("lse", lse, torch.float32, (B, Hq)), ("k_stored", k_stored, bf, (B, Hkv, d)),
-        ("v_stored", v_stored, bf, (B, Hkv, d)),
-        ("workspace", workspace, workspace.dtype, tuple(workspace.shape))])
-    _kv4_call(kv4.device, load().yr_attn_decode_kv4,
-              (_ptr(q_new), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(cache_len), _ptr(out),
-               _ptr(lse), _ptr(k_stored), _ptr(v_stored), B, Hq, Hkv, d, T_max,
-               ctypes.byref(table), int(window), int(n_sink), _ptr(workspace),
-               workspace.numel() * workspace.element_size()), stream)
+                                dtype=torch.uint8, device=dev)
+    sq, sk = (B, Hq, d), (B, Hkv, d)
+    _kv4_call(dev, load().yr_attn_decode_kv4,
+              (_kv4_arg(fn, "q_new", q_new, dev, bf, sq), _kv4_arg(fn, "k_new", k_new, dev, bf, sk),
+               _kv4_arg(fn, "v_new", v_new, dev, bf, sk), kv4.data_ptr(),
+               _kv4_arg(fn, "cache_len", cache_len, dev, torch.int32, (B,)),
+               _kv4_arg(fn, "out", out, dev, bf, sq),
+               _kv4_arg(fn, "lse", lse, dev, torch.float32, (B, Hq)),
+               _kv4_arg(fn, "k_stored", k_stored, dev, bf, sk),
+               _kv4_arg(fn, "v_stored", v_stored, dev, bf, sk), B, Hq, Hkv, d, T_max,
+               ctypes.byref(table), int(window), int(n_sink)) +
+              _kv4_workspace(fn, workspace, dev), stream)
     return out
 
 
@@ -599,24 +618,24 @@ def attn_prefill_chunk_kv4(q, k_new, v_new, kv4, P0: int, table: RopeTable, wind
     """Chunked prefill over the 4-bit cache: q [B,Hq,Tq,d], k_new/v_new [B,Hkv,Tq,d] bf16 at
     positions P0.. .  Writes slots P0..P0+Tq-1 and attends over slots 0..P0+Tq-1 as the cache
     holds them; returns the output [B,Hq,Tq,d] bf16.  lse fp32 [B,Hq,Tq] is filled if given."""
+    fn, bf = "attn_prefill_chunk_kv4", torch.bfloat16
     B, Hq, Tq, d = q.shape
     Hkv, T_max = kv4.shape[1], kv4.shape[2]
+    dev = _kv4_cache_of(fn, kv4, B, Hkv, d)
     if out is None:
-        out = torch.empty((B, Hq, Tq, d), dtype=torch.bfloat16, device=kv4.device)
+        out = torch.empty((B, Hq, Tq, d), dtype=bf, device=dev)
     if workspace is None:
         workspace = torch.empty(
             attn_prefill_chunk_kv4_workspace_bytes(B, Hq, Hkv, Tq, d, int(P0)),
-            dtype=torch.uint8, device=kv4.device)
-    bf = torch.bfloat16
-    _kv4_tensors("attn_prefill_chunk_kv4", kv4, [
-        ("kv4", kv4, torch.uint8, (B, Hkv, T_max, 5 * d // 4)), ("q", q, bf, (B, Hq, Tq, d)),
-        ("k_new", k_new, bf, (B, Hkv, Tq, d)), ("v_new", v_new, bf, (B, Hkv, Tq, d)),
-        ("out", out, bf, (B, Hq, Tq, d)), ("lse", lse, torch.float32, (B, Hq, Tq)),
-        ("workspace", workspace, workspace.dtype, tuple(workspace.shape))])
-    _kv4_call(kv4.device, load().yr_attn_prefill_chunk_kv4,
-              (_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(kv4), _ptr(out), _ptr(lse), B, Hq, Hkv, Tq,
-               d, int(P0), T_max, ctypes.byref(table), int(window), int(n_sink),
-               _ptr(workspace), workspace.numel() * workspace.element_size()), stream)
+            dtype=torch.uint8, device=dev)
+    sq, sk = (B, Hq, Tq, d), (B, Hkv, Tq, d)
+    _kv4_call(dev, load().yr_attn_prefill_chunk_kv4,
+              (_kv4_arg(fn, "q", q, dev, bf, sq), _kv4_arg(fn, "k_new", k_new, dev, bf, sk),
+               _kv4_arg(fn, "v_new", v_new, dev, bf, sk), kv4.data_ptr(),
+               _kv4_arg(fn, "out", out, dev, bf, sq),
+               _kv4_arg(fn, "lse", lse, dev, torch.float32, (B, Hq, Tq)), B, Hq, Hkv, Tq, d,
+               int(P0), T_max, ctypes.byref(table), int(window), int(n_sink)) +
+              _kv4_workspace(fn, workspace, dev), stream)
     return out
 
 

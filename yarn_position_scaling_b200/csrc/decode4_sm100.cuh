@@ -59,26 +59,43 @@ __device__ __forceinline__ DecRanges dec4_ranges(const Decode4Params &p, int L) 
     return r;
 }
 
-// The partition, as every block derives it from cache_len.  A segment is kDec4Lead units
-// for what a block does once for it (query, partial result) and one for each key, so that
-// blocks of many short segments and blocks of few long ones take equally long.
-__device__ __forceinline__ long long dec4_units_per_block(const Decode4Params &p, long long total) {
-    const long long even = (total + p.grid_blocks - 1) / p.grid_blocks;
-    return even > kDec4Chunk + kDec4Lead ? even : kDec4Chunk + kDec4Lead;
-}
-// Units of a segment with `keys` visible keys: none for a length outside the cache.
-__device__ __forceinline__ long long dec4_seg_units(long long keys) { return keys > 0 ? keys + kDec4Lead : 0; }
-__device__ __forceinline__ long long dec4_seq_units(const Decode4Params &p, int b) {
-    if (b >= p.B) return 0;
+// The partition, as every block derives it from cache_len.  A segment is `lead` units for
+// what a block does once for it (query, partial result) and one for each key, so that blocks
+// of many short segments and blocks of few long ones take equally long; where there are
+// few keys for the blocks it is 0, and each takes as few keys as it may.
+struct Dec4Plan {
+    long long U;  // units of a block
+    int lead;
+};
+__device__ __forceinline__ int dec4_keys(const Decode4Params &p, int b) {
     const DecRanges r = dec4_ranges(p, p.cache_len[b]);
-    return p.Hkv * dec4_seg_units(static_cast<long long>(r.len1) + r.len2);
+    return r.len1 + r.len2;
 }
-__device__ __forceinline__ long long dec4_total(const Decode4Params &p, int lane) {
-    long long t = 0;
-    for (int b = lane; b < p.B; b += 32) t += dec4_seq_units(p, b);
+// Units of a segment: none for a length outside the cache.
+__device__ __forceinline__ long long dec4_units(int keys, int lead) {
+    return keys > 0 ? static_cast<long long>(keys) + lead : 0;
+}
+// Called by a full warp.
+__device__ __forceinline__ Dec4Plan dec4_plan(const Decode4Params &p, int lane) {
+    long long keys = 0;
+    int segs = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const int n = dec4_keys(p, b);
+        keys += n;
+        segs += n > 0;
+    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    return t;
+    for (int off = 16; off > 0; off >>= 1) {
+        keys += __shfl_xor_sync(0xffffffffu, keys, off);
+        segs += __shfl_xor_sync(0xffffffffu, segs, off);
+    }
+    keys *= p.Hkv;
+    Dec4Plan plan;
+    plan.lead = keys >= static_cast<long long>(kDec4Chunk) * p.grid_blocks ? kDec4Lead : 0;
+    const long long total = keys + static_cast<long long>(segs) * p.Hkv * plan.lead;
+    const long long even = (total + p.grid_blocks - 1) / p.grid_blocks;
+    plan.U = even > kDec4Chunk ? even : kDec4Chunk;
+    return plan;
 }
 
 // The new row: rotated, quantised, into slot L of the cache, and its values to k_stored and
@@ -175,6 +192,7 @@ struct Decode4Smem {
     alignas(128) uint8_t ring[kDec4Warps][kDec4Stages][kStageBytes];  // also the warps' outputs
     alignas(16) uint8_t new_row[kv4_row_bytes(HD)];
     double2 cs[HD / 2];
+    float2 q_cs[HD / 2];
     uint4 q_hi[8 * NT][HD / 8], q_lo[8 * NT][HD / 8];  // fragments, see the rotation below
     float q_sum[8 * NT][HD / kKv4Group];  // sums of the scaled query over the groups
     float q_scale[8 * NT];  // what takes the scaled query back
@@ -224,21 +242,12 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     const int key_at = dec4_key<HD>(c) * kRow;
     const int val_at0 = dec4_key<HD>(2 * r) * kRow + HD / 2 + (G == 4 ? 8 : 4) * c;
     const int val_at1 = dec4_key<HD>(2 * r + 1) * kRow + HD / 2 + (G == 4 ? 8 : 4) * c;
-    const long long total = dec4_total(p, lane);
-    const long long U = dec4_units_per_block(p, total);
-    const long long u_lo = static_cast<long long>(blockIdx.x) * U;
-    const long long u_hi = min(u_lo + U, total);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Dec4Plan plan = dec4_plan(p, lane);
+    const long long u_lo = blockIdx.x * plan.U, u_hi = u_lo + plan.U;
     if (blockIdx.x == 0 && tid == 0)
         for (int b = 0; b < p.B; ++b)
             if (p.cache_len[b] < 0 || p.cache_len[b] > p.T_max - 1) raise_status(kStatusBadCacheLen);
-    if (u_lo >= u_hi) return;
-    if (tid == 0) {
-        for (int w = 0; w < kDec4Warps; ++w)
-            for (int s = 0; s < kDec4Stages; ++s) mbar_init(&sm->full[w][s], 1);
-        sm->abort = 0;
-        fence_mbar_init();
-    }
-    __syncthreads();
     // This warp's ring, over all segments: the stages of the next copy and the next wait,
     // and the parity of the latter.
     uint32_t s_load = 0, s_wait = 0, parity = 0;
@@ -247,18 +256,27 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     // Sequences before the first one of this block.
     int b = 0;
     long long seg0 = 0;
-    for (long long v; b < p.B && seg0 + (v = dec4_seq_units(p, b)) <= u_lo; ++b) seg0 += v;
+    for (long long v; b < p.B && seg0 + (v = p.Hkv * dec4_units(dec4_keys(p, b), plan.lead)) <= u_lo; ++b)
+        seg0 += v;
+    if (b == p.B) return;
+    if (tid == 0) {
+        for (int w = 0; w < kDec4Warps; ++w)
+            for (int s = 0; s < kDec4Stages; ++s) mbar_init(&sm->full[w][s], 1);
+        sm->abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
     for (; b < p.B && seg0 < u_hi; ++b) {
         const int L = p.cache_len[b];
         const DecRanges rg = dec4_ranges(p, L);
-        const long long V = dec4_seg_units(static_cast<long long>(rg.len1) + rg.len2);
+        const long long V = dec4_units(rg.len1 + rg.len2, plan.lead);
         if (V == 0) continue;
         int kvh = seg0 < u_lo ? static_cast<int>((u_lo - seg0) / V) : 0;
         seg0 += kvh * V;
         for (; kvh < p.Hkv && seg0 < u_hi; ++kvh, seg0 += V) {
             // Units [u0, u1) of the segment's keys are this block's: keys of the first
             // range, then of the second.
-            const long long k0 = seg0 + kDec4Lead;
+            const long long k0 = seg0 + plan.lead;
             const int u0 = static_cast<int>(max(u_lo, k0) - k0);
             const int u1 = static_cast<int>(min(u_hi, seg0 + V) - k0);
             if (u1 <= 0) continue;
@@ -304,16 +322,57 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 if (ld_key < ld_end) load();
 
             // ---- queries: rotated, scaled, as fragments of two fp16 parts
-            for (int i = tid; i < HD / 2; i += kDec4Threads) sm->cs[i] = kv4_cos_sin(L, p.turns[i]);
-            __syncthreads();
-            for (int i = tid; i < 8 * NT * (HD / 8); i += kDec4Threads) {
-                const int h = i / (HD / 8), ch = i % (HD / 8);
-                float y[8], mx = 0.f;
+            constexpr int kItems = 8 * NT * (HD / 8);  // chunks of eight elements
+            constexpr int kPer = (kItems + kDec4Threads - 1) / kDec4Threads;
+            uint4 raw[kPer], other[kPer];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = 0.f;
-                if (h < g)
-                    kv4_rotate8<HD, kHalf>(p.q_new + (static_cast<long long>(b) * p.Hq + kvh * g + h) * HD,
-                                           ch, sm->cs, y);
+            for (int n = 0; n < kPer; ++n) {
+                const int i = tid + n * kDec4Threads, h = i / (HD / 8), ch = i % (HD / 8);
+                raw[n] = other[n] = make_uint4(0, 0, 0, 0);
+                if (i < kItems && h < g) {
+                    const uint4 *row = reinterpret_cast<const uint4 *>(
+                        p.q_new + (static_cast<long long>(b) * p.Hq + kvh * g + h) * HD);
+                    raw[n] = __ldg(row + ch);
+                    if (kHalf) other[n] = __ldg(row + (ch ^ (HD / 16)));
+                }
+            }
+            // The new row wants its sines in 64 bits; the queries' 22 bits do with fp32 ones.
+            for (int i = tid; i < HD / 2; i += kDec4Threads) {
+                if (has_L) {
+                    const double2 t = kv4_cos_sin(L, p.turns[i]);
+                    sm->cs[i] = t;
+                    sm->q_cs[i] = make_float2(static_cast<float>(t.x), static_cast<float>(t.y));
+                } else {
+                    const double tr = static_cast<double>(L) * p.turns[i];
+                    float sn, co;
+                    sincospif(2.f * static_cast<float>(tr - rint(tr)), &sn, &co);
+                    sm->q_cs[i] = make_float2(co, sn);
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < kPer; ++n) {
+                const int i = tid + n * kDec4Threads, h = i / (HD / 8), ch = i % (HD / 8);
+                if (i >= kItems) break;
+                float x[8], y[8], mx = 0.f;
+                unpack_bf16x8(raw[n], x);
+                if constexpr (kHalf) {
+                    float z[8];
+                    unpack_bf16x8(other[n], z);
+                    const int c0 = 8 * (ch % (HD / 16));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 t = sm->q_cs[c0 + e];
+                        y[e] = ch < HD / 16 ? x[e] * t.x - z[e] * t.y : z[e] * t.y + x[e] * t.x;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 t = sm->q_cs[4 * ch + e];
+                        y[2 * e] = x[2 * e] * t.x - x[2 * e + 1] * t.y;
+                        y[2 * e + 1] = x[2 * e] * t.y + x[2 * e + 1] * t.x;
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(y[e]));
 #pragma unroll
@@ -350,6 +409,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                                            : 0.f;
                 }
             }
+            __syncthreads();
+            // The warp whose tile ends with the new row makes it meanwhile.
             const int tile_L = hi2 > lo2 ? n_t1 + (L - lo2) / kDec4Tile : (L - lo1) / kDec4Tile;
             if (has_L && warp == (tile_L & (kDec4Warps - 1))) {
                 dec4_append<HD, kHalf>(p, b, kvh, sm->new_row, sm->cs, lane);
@@ -358,7 +419,6 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                     reinterpret_cast<uint4 *>(plane + static_cast<long long>(L) * kRow)[lane] =
                         reinterpret_cast<const uint4 *>(sm->new_row)[lane];
             }
-            __syncthreads();
             // Of the two parts, this column's with copies, else both (from shared memory, in
             // the loop: registers are short).
             uint4 q_reg[G];
@@ -726,38 +786,84 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
 }
 
 // One block per (query head, sequence): the pieces of its segment, by log-sum-exp weights.
+// Four warps share the pieces, a lane holding HD/32 dims, so that few loads follow one another
+// (one warp's turn through 40 pieces took 8 us, this 3).
+constexpr int kDec4MergeThreads = 128;
 template <int HD>
-__global__ void __launch_bounds__(HD) decode4_merge_kernel(const __grid_constant__ Decode4Params p) {
-    const int hq = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq, dim = threadIdx.x;
+__global__ void __launch_bounds__(kDec4MergeThreads) decode4_merge_kernel(const __grid_constant__ Decode4Params p) {
+    constexpr int kVec = HD / 32, kWarps = kDec4MergeThreads / 32;
+    __shared__ float weight[kDec4MaxBlocks];
+    __shared__ float red[kWarps], out[kWarps][HD];
+    const int hq = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int L = p.cache_len[b], g = p.group, kvh = hq / g, hh = hq % g;
     const long long oi = static_cast<long long>(b) * p.Hq + hq;
     const DecRanges rg = dec4_ranges(p, L);
-    const long long V = dec4_seg_units(static_cast<long long>(rg.len1) + rg.len2);
-    if (V == 0) {  // a length outside the cache
-        p.o[oi * HD + dim] = __float2bfloat16(__int_as_float(0x7fc00000));
-        if (p.lse != nullptr && dim == 0) p.lse[oi] = __int_as_float(0x7fc00000);
+    if (rg.len1 + rg.len2 == 0) {  // a length outside the cache
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (tid < HD) p.o[oi * HD + tid] = __float2bfloat16(__int_as_float(0x7fc00000));
+        if (p.lse != nullptr && tid == 0) p.lse[oi] = __int_as_float(0x7fc00000);
         return;
     }
-    const int lane = dim & 31;
-    const long long U = dec4_units_per_block(p, dec4_total(p, lane));
+    const Dec4Plan plan = dec4_plan(p, lane);
     long long seg0 = 0;
-    for (int i = lane; i < b; i += 32) seg0 += dec4_seq_units(p, i);
+    for (int i = lane; i < b; i += 32) seg0 += p.Hkv * dec4_units(dec4_keys(p, i), plan.lead);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) seg0 += __shfl_xor_sync(0xffffffffu, seg0, off);
+    const long long V = dec4_units(rg.len1 + rg.len2, plan.lead);
     seg0 += kvh * V;
-    const int first = static_cast<int>((seg0 + kDec4Lead) / U), last = static_cast<int>((seg0 + V - 1) / U);
-    const long long seg = static_cast<long long>(b) * p.Hkv + kvh;
-    float M = -INFINITY;
-    for (int i = first; i <= last; ++i) M = fmaxf(M, p.ws_ml[((i + seg) * g + hh) * 2]);
-    float acc = 0.f, sum = 0.f;
-    for (int i = first; i <= last; ++i) {
-        const long long s = (i + seg) * g + hh;
-        const float w = M == -INFINITY ? 0.f : ex2f(p.ws_ml[s * 2] - M);
-        sum += w * p.ws_ml[s * 2 + 1];
-        acc += w * p.ws_o[s * HD + dim];
+    const int first = static_cast<int>((seg0 + plan.lead) / plan.U);
+    const int n = static_cast<int>((seg0 + V - 1) / plan.U) - first + 1;  // pieces, at most one a block
+    const long long slot0 = (first + static_cast<long long>(b) * p.Hkv + kvh) * g + hh;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's results
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
+    float M = -INFINITY, sum = 0.f;
+    for (int i = tid; i < n; i += kDec4MergeThreads) {
+        weight[i] = ml[slot0 + static_cast<long long>(i) * g].x;
+        M = fmaxf(M, weight[i]);
     }
-    p.o[oi * HD + dim] = __float2bfloat16_rn(acc / sum);
-    if (p.lse != nullptr && dim == 0) p.lse[oi] = (M + log2f(sum)) * 0.69314718055994531f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[w]);
+    float acc[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < n; i += kWarps) {
+        const long long s = slot0 + static_cast<long long>(i) * g;
+        const float w = M == -INFINITY ? 0.f : ex2f(weight[i] - M);
+        const float *o = p.ws_o + s * HD + kVec * lane;
+        sum = fmaf(w, ml[s].y, sum);
+        if constexpr (kVec == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(o);
+            acc[0] = fmaf(w, v.x, acc[0]);
+            acc[1] = fmaf(w, v.y, acc[1]);
+            acc[2] = fmaf(w, v.z, acc[2]);
+            acc[3] = fmaf(w, v.w, acc[3]);
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(o);
+            acc[0] = fmaf(w, v.x, acc[0]);
+            acc[1] = fmaf(w, v.y, acc[1]);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) out[warp][kVec * lane + e] = acc[e];
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += red[w];
+    if (tid < HD) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += out[w][tid];
+        p.o[oi * HD + tid] = __float2bfloat16_rn(v / sum);
+    }
+    if (p.lse != nullptr && tid == 0) p.lse[oi] = (M + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace yr

@@ -263,12 +263,20 @@ extern "C" int yr_attn_decode_kv4(const void *q_new, const void *k_new, const vo
          : half   ? launch_decode4<64, true>(dp, sm_count, st)
                   : launch_decode4<64, false>(dp, sm_count, st);
     if (rc != YR_OK) return rc;
-    const unsigned merge = static_cast<unsigned>(B) * Hq;
-    if (d == 128)
-        yr::decode4_merge_kernel<128><<<merge, 128, 0, st>>>(dp);
-    else
-        yr::decode4_merge_kernel<64><<<merge, 64, 0, st>>>(dp);
-    cudaError_t e = cudaGetLastError();
+    // The merge may start, and find its pieces, while the split kernel still runs; it waits
+    // for that kernel's results itself.
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(B) * Hq);
+    cfg.blockDim = dim3(yr::kDec4MergeThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = d == 128 ? cudaLaunchKernelEx(&cfg, yr::decode4_merge_kernel<128>, dp)
+                                   : cudaLaunchKernelEx(&cfg, yr::decode4_merge_kernel<64>, dp);
     if (e != cudaSuccess) return cuda_fail("decode4_merge_kernel launch", e);
     return YR_OK;
 }
