@@ -48,7 +48,7 @@ int launch_kv4_write(const void *k, const void *v, void *kv4, int B, int Hkv, in
     wp.counts = counts;
     wp.B = B; wp.Hkv = Hkv; wp.T = T; wp.T_max = T_max; wp.pos0 = pos0;
     for (int i = 0; i < d / 2; ++i) wp.turns[i] = tab->turns[i];
-    const int rows = yr::kKv4Threads / (d / 8);
+    const int rows = yr::kKv4WriteRows;
     const long long tiles = (static_cast<long long>(T) + rows - 1) / rows;
     // All heads of a row in one block where the rows alone fill the GPU, else spread.
     int split = 1;
@@ -57,13 +57,13 @@ int launch_kv4_write(const void *k, const void *v, void *kv4, int B, int Hkv, in
     const dim3 grid(static_cast<unsigned>(tiles), B, (Hkv + wp.heads - 1) / wp.heads);
     const bool half = tab->pairs == YR_PAIR_HALF;
     if (d == 128 && half)
-        yr::kv4_write_kernel<128, true><<<grid, yr::kKv4Threads, 0, st>>>(wp);
+        yr::kv4_write_kernel<128, true><<<grid, yr::kKv4WriteThreads, 0, st>>>(wp);
     else if (d == 128)
-        yr::kv4_write_kernel<128, false><<<grid, yr::kKv4Threads, 0, st>>>(wp);
+        yr::kv4_write_kernel<128, false><<<grid, yr::kKv4WriteThreads, 0, st>>>(wp);
     else if (half)
-        yr::kv4_write_kernel<64, true><<<grid, yr::kKv4Threads, 0, st>>>(wp);
+        yr::kv4_write_kernel<64, true><<<grid, yr::kKv4WriteThreads, 0, st>>>(wp);
     else
-        yr::kv4_write_kernel<64, false><<<grid, yr::kKv4Threads, 0, st>>>(wp);
+        yr::kv4_write_kernel<64, false><<<grid, yr::kKv4WriteThreads, 0, st>>>(wp);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("kv4_write_kernel launch", e);
     return YR_OK;
@@ -71,20 +71,20 @@ int launch_kv4_write(const void *k, const void *v, void *kv4, int B, int Hkv, in
 
 int launch_kv4_read(yr::Kv4ReadParams rp, int d, bool f16, int sm_count, cudaStream_t st) {
     const long long rows = rp.n_head + (static_cast<long long>(rp.T) - rp.skip_to);
-    const int per_block = yr::kKv4Threads / (d / 8);
+    const int per_block = yr::kKv4ReadThreads / 4;
     long long blocks = (rows + per_block - 1) / per_block;
     const long long planes = static_cast<long long>(rp.B) * rp.Hkv;
     const long long cap = (16ll * sm_count + planes - 1) / planes;
     if (blocks > cap) blocks = cap;
     const dim3 grid(static_cast<unsigned>(blocks), rp.Hkv, rp.B);
     if (d == 128 && f16)
-        yr::kv4_read_kernel<128, true><<<grid, yr::kKv4Threads, 0, st>>>(rp);
+        yr::kv4_read_kernel<128, true><<<grid, yr::kKv4ReadThreads, 0, st>>>(rp);
     else if (d == 128)
-        yr::kv4_read_kernel<128, false><<<grid, yr::kKv4Threads, 0, st>>>(rp);
+        yr::kv4_read_kernel<128, false><<<grid, yr::kKv4ReadThreads, 0, st>>>(rp);
     else if (f16)
-        yr::kv4_read_kernel<64, true><<<grid, yr::kKv4Threads, 0, st>>>(rp);
+        yr::kv4_read_kernel<64, true><<<grid, yr::kKv4ReadThreads, 0, st>>>(rp);
     else
-        yr::kv4_read_kernel<64, false><<<grid, yr::kKv4Threads, 0, st>>>(rp);
+        yr::kv4_read_kernel<64, false><<<grid, yr::kKv4ReadThreads, 0, st>>>(rp);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("kv4_read_kernel launch", e);
     return YR_OK;

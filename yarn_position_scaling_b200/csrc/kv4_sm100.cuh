@@ -161,47 +161,229 @@ __device__ __forceinline__ void kv4_store8(uint8_t *row, int c, uint32_t kw, __h
     }
 }
 
-constexpr int kKv4Threads = 256;
+// ------------------------------------------------------------------------------- write
+// Four lanes hold a row: lane r the elements 32g + 8r .. + 7 of every group g.  Both elements
+// of a pair are then the same lane's in either pair layout, a group's extremes are two
+// shuffles away, and a lane's codes of a row are 16 neighbouring bytes of it.
+constexpr int kKv4WriteRows = 32;  // rows of a block
+constexpr int kKv4WriteThreads = 4 * kKv4WriteRows;
 
-// A block takes kRows rows of one sequence and `heads` KV heads in turn, so that the fp64
-// sines of a position are computed once for its heads; a lane takes eight elements.
+// The high word of a bf16 number (in the upper half of `bits`, zeros below) as fp64, in integer
+// arithmetic (the conversion instruction runs at an eighth of the rate).  Zeros become 2^-127,
+// which no later rounding sees; infinities and NaN become numbers beyond the fp32 range, which
+// the range check then finds.
+__device__ __forceinline__ double bf16_as_double(uint32_t bits) {
+    const uint32_t hi = (static_cast<uint32_t>(static_cast<int32_t>(bits) >> 3) & 0x8fffffffu) + (896u << 20);
+    return __hiloint2double(static_cast<int>(hi), 0);
+}
+__device__ __forceinline__ void unpack_double8(const uint4 &raw, double (&x)[8]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_as_double(w[i] << 16);
+        x[2 * i + 1] = bf16_as_double(w[i] & 0xffff0000u);
+    }
+}
+// Pair (a, b) turned by the angle of t = (cos, sin), rounded to fp32 once.
+__device__ __forceinline__ void kv4_turn(double a, double b, const double2 &t, float &ya, float &yb) {
+    ya = static_cast<float>(fma(a, t.x, -__dmul_rn(b, t.y)));
+    yb = static_cast<float>(fma(a, t.y, __dmul_rn(b, t.x)));
+}
+
+// Codes of one row from the elements of its four lanes: w[g] this lane's eight of group g, and
+// `sz` the (s, z) of group r (lanes r < G).  The extremes are reduced so that lane r ends with
+// those of group r, which then does that group's divisions for all four.  A code is
+// rint(15 sat((x - z) / (15 s))) by a product with the reciprocal, off by less than 4e-6, and
+// by the division where the quotient is that near a border; the codes of a word are added up
+// with the bits of the rounding constant and the constants taken off at the end.
+template <int G>
+__device__ __forceinline__ void kv4_quantise_row(const float (&x)[G][8], int r, uint32_t (&w)[G], __half2 &sz) {
+    float lo[G], hi[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        lo[g] = fminf(x[g][0], x[g][1]);
+        hi[g] = fmaxf(x[g][0], x[g][1]);
+#pragma unroll
+        for (int i = 2; i < 8; i += 2) {
+            lo[g] = fminf(lo[g], fminf(x[g][i], x[g][i + 1]));
+            hi[g] = fmaxf(hi[g], fmaxf(x[g][i], x[g][i + 1]));
+        }
+    }
+    if constexpr (G == 4) {  // lanes r and r ^ 2 take over groups r & 2 and (r & 2) + 1
+        const bool up = (r & 2) != 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const float l = __shfl_xor_sync(0xffffffffu, up ? lo[g] : lo[g + 2], 2);
+            const float h = __shfl_xor_sync(0xffffffffu, up ? hi[g] : hi[g + 2], 2);
+            lo[g] = fminf(up ? lo[g + 2] : lo[g], l);
+            hi[g] = fmaxf(up ? hi[g + 2] : hi[g], h);
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            lo[g] = fminf(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], 2));
+            hi[g] = fmaxf(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], 2));
+        }
+    }
+    const bool odd = (r & 1) != 0;
+    const float l = __shfl_xor_sync(0xffffffffu, odd ? lo[0] : lo[1], 1);
+    const float h = __shfl_xor_sync(0xffffffffu, odd ? hi[0] : hi[1], 1);
+    const __half z16 = __float2half_rn(fminf(odd ? lo[1] : lo[0], l));
+    const __half s16 = __float2half_rn(
+        fmaxf(__fdiv_rn(__fsub_rn(fmaxf(odd ? hi[1] : hi[0], h), __half2float(z16)), 15.f), 0.f));
+    sz = __halves2half2(s16, z16);
+    const float s_own = __half2float(s16);
+    const float inv_own = s_own > 0.f ? __fdividef(1.f, 15.f * s_own) : 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const __half2 szg = __shfl_sync(0xffffffffu, sz, g, 4);
+        const float inv = __shfl_sync(0xffffffffu, inv_own, g, 4);
+        const float z = __high2float(szg);
+        uint32_t word = 0u - 0x4B400000u * 0x11111111u;
+        float far = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = __saturatef(__fsub_rn(x[g][i], z) * inv);
+            const float t = fmaf(q, 15.f, 12582912.f);
+            far = fmaxf(far, fabsf(fmaf(q, 15.f, 12582912.f - t)));
+            word += __float_as_uint(t) << (4 * i);
+        }
+        if (far > 0.49999f) {
+            const float s = __low2float(szg);
+            word = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float n = rintf(__fdiv_rn(__fsub_rn(x[g][i], z), s));
+                word |= static_cast<uint32_t>(fminf(fmaxf(n, 0.f), 15.f)) << (4 * i);
+            }
+        }
+        w[g] = word;
+    }
+}
+
+// A block takes 32 rows of one sequence and `heads` KV heads in turn, and computes the sines
+// of its positions once for them: by angle addition from row to row, 16 (8) rows from a start
+// that is computed (16 products cost 2^-49).
 template <int HD, bool kHalf>
-__global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
-    constexpr int kLanes = HD / 8;  // lanes of a row
-    constexpr int kRows = kKv4Threads / kLanes;
-    __shared__ double2 cs[kRows][HD / 2];
+__global__ void __launch_bounds__(kKv4WriteThreads) kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
+    constexpr int G = HD / kKv4Group, kPairs = HD / 2, kRows = kKv4WriteRows;
+    // Pair 4r + i (8r + i) of a group stands at 4i + r, and a row's end is 64 bytes longer than
+    // a multiple of 128: the 16-byte reads of two rows' lanes then cover every bank once.
+    constexpr int kLane = kHalf ? 8 : 4;
+    __shared__ double2 cs[kRows][kPairs + 4];
     const int b = blockIdx.y;
     int first;
     const int n = kv4_rows_of(p, b, first);
     const int t0 = static_cast<int>(blockIdx.x) * kRows;
     if (t0 >= n) return;
-    for (int i = threadIdx.x; i < kRows * (HD / 2); i += kKv4Threads)
-        cs[i / (HD / 2)][i % (HD / 2)] =
-            kv4_cos_sin(first + t0 + i / (HD / 2), p.turns[i % (HD / 2)]);
+    {
+        constexpr int kRun = kRows * kPairs / kKv4WriteThreads;  // rows of a thread
+        const int pair = threadIdx.x % kPairs, row0 = threadIdx.x / kPairs * kRun;
+        const int at = pair / (4 * kLane) * (4 * kLane) + 4 * (pair % kLane) + pair / kLane % 4;
+        const double2 step = kv4_cos_sin(1, p.turns[pair]);
+        double2 u = kv4_cos_sin(first + t0 + row0, p.turns[pair]);
+        cs[row0][at] = u;
+#pragma unroll
+        for (int i = 1; i < kRun; ++i) {
+            u = make_double2(fma(u.x, step.x, -__dmul_rn(u.y, step.y)), fma(u.x, step.y, __dmul_rn(u.y, step.x)));
+            cs[row0 + i][at] = u;
+        }
+    }
     __syncthreads();
-    const int r = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
-    const int t = t0 + r;
-    const bool live = t < n;
-    const long long tl = live ? t : n - 1;  // idle lanes repeat the last row, without a store
+    const int row = threadIdx.x / 4, r = threadIdx.x % 4;
+    const bool live = t0 + row < n;
+    const int at = live ? row : n - 1 - t0;  // idle lanes repeat the last row, without a store
+    const long long t = t0 + at;
     const int h0 = blockIdx.z * p.heads, h1 = min(h0 + p.heads, p.Hkv);
     bool bad = false;
     for (int h = h0; h < h1; ++h) {
-        float y[8], x[8];
-        kv4_rotate8<HD, kHalf>(p.k + b * p.ksb + h * p.ksh + tl * p.kst, c,
-                               cs[live ? r : n - 1 - t0], y);
-        unpack_bf16x8(__ldg(reinterpret_cast<const uint4 *>(p.v + b * p.vsb + h * p.vsh +
-                                                            tl * p.vst + 8 * c)), x);
+        uint4 kr[G], vr[G];
+        const uint4 *krow = reinterpret_cast<const uint4 *>(p.k + b * p.ksb + h * p.ksh + t * p.kst) + r;
+        const uint4 *vrow = reinterpret_cast<const uint4 *>(p.v + b * p.vsb + h * p.vsh + t * p.vst) + r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) bad |= kv4_clamp(y[i]) | kv4_clamp(x[i]);
-        __half2 ksz, vsz;
-        const uint32_t kw = kv4_quantise8(y, ksz), vw = kv4_quantise8(x, vsz);
-        if (live)
-            kv4_store8<HD>(p.kv4 + ((static_cast<long long>(b) * p.Hkv + h) * p.T_max + first + t) *
-                                       kv4_row_bytes(HD), c, kw, ksz, vw, vsz);
+        for (int g = 0; g < G; ++g) {
+            kr[g] = __ldg(krow + 4 * g);
+            vr[g] = __ldg(vrow + 4 * g);
+        }
+        uint8_t *to = p.kv4 + ((static_cast<long long>(b) * p.Hkv + h) * p.T_max + first + t) * kv4_row_bytes(HD);
+        float x[G][8];
+        uint32_t w[G];
+        __half2 sz;
+        // Values outside the fp16 range, rare, are brought into it and reported.
+        auto clamp = [&] {
+            float top = 0.f;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[g][i]));
+            if (top >= kF16RoundsFinite) {
+                bad = true;
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) kv4_clamp(x[g][i]);
+            }
+        };
+        if constexpr (kHalf) {
+#pragma unroll
+            for (int g = 0; g < G / 2; ++g) {
+                double a[8], c[8];
+                unpack_double8(kr[g], a);
+                unpack_double8(kr[g + G / 2], c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    kv4_turn(a[i], c[i], cs[at][32 * g + 4 * i + r], x[g][i], x[g + G / 2][i]);
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                double a[8];
+                unpack_double8(kr[g], a);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    kv4_turn(a[2 * i], a[2 * i + 1], cs[at][16 * g + 4 * i + r], x[g][2 * i], x[g][2 * i + 1]);
+            }
+        }
+        clamp();
+        kv4_quantise_row<G>(x, r, w, sz);
+        if (live) {
+            if constexpr (G == 4)
+                *reinterpret_cast<uint4 *>(to + 16 * r) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+                *reinterpret_cast<uint2 *>(to + 8 * r) = make_uint2(w[0], w[1]);
+            if (r < G) reinterpret_cast<__half2 *>(to + HD)[r] = sz;
+        }
+        uint32_t over = 0;  // top bits of halves whose magnitude is 65536 or more, or NaN
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            unpack_bf16x8(vr[g], x[g]);
+            over |= ((vr[g].x & 0x7fff7fffu) + 0x38803880u) | ((vr[g].y & 0x7fff7fffu) + 0x38803880u) |
+                    ((vr[g].z & 0x7fff7fffu) + 0x38803880u) | ((vr[g].w & 0x7fff7fffu) + 0x38803880u);
+        }
+        if (over & 0x80008000u) {
+            bad = true;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) kv4_clamp(x[g][i]);
+        }
+        kv4_quantise_row<G>(x, r, w, sz);
+        if (live) {
+            // Value units 2r and 2r + 1 of every group: the words' halves, regrouped.
+            if constexpr (G == 4)
+                *reinterpret_cast<uint4 *>(to + HD / 2 + 16 * r) =
+                    make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410),
+                               __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632));
+            else
+                *reinterpret_cast<uint2 *>(to + HD / 2 + 8 * r) =
+                    make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632));
+            if (r < G) reinterpret_cast<__half2 *>(to + HD + 4 * G)[r] = sz;
+        }
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) raise_status(kStatusKv4Range);
 }
 
+// -------------------------------------------------------------------------------- read
 // Eight codes of a lane as values.
 __device__ __forceinline__ void kv4_values8(uint32_t w, __half2 sz, float (&x)[8]) {
     const float s = __low2float(sz), z = __high2float(sz);
@@ -221,40 +403,58 @@ __device__ __forceinline__ uint4 kv4_pack16(float (&x)[8]) {
     }
 }
 
-// A lane takes eight elements of a row; a grid-stride loop over the rows to read.
+constexpr int kKv4ReadThreads = 256;
+
+// Four lanes hold a row as in the write: 16 (8) neighbouring bytes of key and of value codes
+// each, and 16-byte stores of which four lanes' are neighbours.  A grid-stride loop over the
+// rows to read.
 template <int HD, bool kF16>
-__global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
-    constexpr int kLanes = HD / 8, G = HD / kKv4Group;
+__global__ void __launch_bounds__(kKv4ReadThreads) kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
+    constexpr int G = HD / kKv4Group;
     const int b = blockIdx.z, h = blockIdx.y;
     int first;
-    const int n = min(kv4_rows_of(p, b, first), p.T);
-    const int c = threadIdx.x % kLanes, g = c >> 2, r = c & 3;
+    const int n = kv4_rows_of(p, b, first);
+    const int r = threadIdx.x % 4;
     const int rows = p.n_head + (p.T - p.skip_to);
-    uint16_t *ko = static_cast<uint16_t *>(p.k), *vo = static_cast<uint16_t *>(p.v);
-    const long long step = static_cast<long long>(gridDim.x) * (kKv4Threads / kLanes);
-    for (long long i = blockIdx.x * static_cast<long long>(kKv4Threads / kLanes) + threadIdx.x / kLanes;
-         i < rows; i += step) {
+    uint4 *ko = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.k) + b * p.ksb + h * p.ksh) + r;
+    uint4 *vo = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.v) + b * p.vsb + h * p.vsh) + r;
+    const uint8_t *plane = p.kv4 + (static_cast<long long>(b) * p.Hkv + h) * p.T_max * kv4_row_bytes(HD);
+    const long long step = static_cast<long long>(gridDim.x) * (kKv4ReadThreads / 4);
+    for (long long i = blockIdx.x * static_cast<long long>(kKv4ReadThreads / 4) + threadIdx.x / 4; i < rows; i += step) {
         const int t = static_cast<int>(i < p.n_head ? i : p.skip_to + (i - p.n_head));
         if (t >= n && !p.zero_rest) continue;
         // A row that becomes zeros reads the plane's first slot, whatever that holds.
         const bool zero = t >= n || (t >= p.zero_lo && t < p.zero_hi);
-        const uint8_t *row = p.kv4 + ((static_cast<long long>(b) * p.Hkv + h) * p.T_max +
-                                      (zero ? 0 : first + t)) * kv4_row_bytes(HD);
-        const __half2 *par = reinterpret_cast<const __half2 *>(row + HD);
-        float x[8];
-        if (ko != nullptr) {
-            kv4_values8(reinterpret_cast<const uint32_t *>(row)[r * G + g], par[g], x);
-            uint4 out = kv4_pack16<kF16>(x);
-            if (zero) out = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(ko + b * p.ksb + h * p.ksh + t * p.kst + 8 * c) = out;
+        const uint8_t *row = plane + (zero ? 0ll : static_cast<long long>(first) + t) * kv4_row_bytes(HD);
+        uint32_t kw[G], vu[G], ksz[G], vsz[G];
+        if constexpr (G == 4) {
+            *reinterpret_cast<uint4 *>(kw) = __ldg(reinterpret_cast<const uint4 *>(row) + r);
+            *reinterpret_cast<uint4 *>(vu) = __ldg(reinterpret_cast<const uint4 *>(row + HD / 2) + r);
+            *reinterpret_cast<uint4 *>(ksz) = __ldg(reinterpret_cast<const uint4 *>(row + HD));
+            *reinterpret_cast<uint4 *>(vsz) = __ldg(reinterpret_cast<const uint4 *>(row + HD) + 1);
+        } else {
+            *reinterpret_cast<uint2 *>(kw) = __ldg(reinterpret_cast<const uint2 *>(row) + r);
+            *reinterpret_cast<uint2 *>(vu) = __ldg(reinterpret_cast<const uint2 *>(row + HD / 2) + r);
+            *reinterpret_cast<uint2 *>(ksz) = __ldg(reinterpret_cast<const uint2 *>(row + HD));
+            *reinterpret_cast<uint2 *>(vsz) = __ldg(reinterpret_cast<const uint2 *>(row + HD) + 1);
         }
-        if (vo != nullptr) {
-            const uint16_t *vu = reinterpret_cast<const uint16_t *>(row + HD / 2);
-            const uint32_t w = vu[(2 * r) * G + g] | (static_cast<uint32_t>(vu[(2 * r + 1) * G + g]) << 16);
-            kv4_values8(w, par[G + g], x);
+        auto put = [&](uint4 *to, uint32_t w, uint32_t sz) {
+            float x[8];
+            kv4_values8(w, *reinterpret_cast<const __half2 *>(&sz), x);
             uint4 out = kv4_pack16<kF16>(x);
             if (zero) out = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(vo + b * p.vsb + h * p.vsh + t * p.vst + 8 * c) = out;
+            *to = out;
+        };
+        if (p.k != nullptr) {
+            uint4 *to = ko + t * (p.kst / 8);
+#pragma unroll
+            for (int g = 0; g < G; ++g) put(to + 4 * g, kw[g], ksz[g]);
+        }
+        if (p.v != nullptr) {
+            uint4 *to = vo + t * (p.vst / 8);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                put(to + 4 * g, __byte_perm(vu[g / 2], vu[G / 2 + g / 2], g & 1 ? 0x7632 : 0x5410), vsz[g]);
         }
     }
 }
