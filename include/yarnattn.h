@@ -502,16 +502,18 @@ int yr_attn_decode_noalloc(const void *q_new, const void *k_new, const void *v_n
  *   fp16 relative to the largest; all sums fp32.
  *
  * attn_prefill_chunk_kv4 -- yr_attn_prefill_chunk over this cache: writes the chunk's rows
- *   into slots P0 .. P0+Tq-1, reads the rows 0 .. P0+Tq-1 back as fp16 into the workspace,
- *   and attends over them.  A chunk's own keys are attended as stored, so the result does
- *   not depend on where a prompt is cut (up to rounding), and Tq = 1 is a decode step.
- *   With a window only the rows that some query of the chunk sees are used.
+ *   into slots P0 .. P0+Tq-1 and attends over the rows 0 .. P0+Tq-1.  A few tokens (up to
+ *   about 30) are taken by the decode kernel, with its precision, over the 4-bit rows; more
+ *   by the prefill kernel, over fp16 copies of the rows that the call makes in the workspace.
+ *   A chunk's own keys are attended as stored, so the result does not depend on where a
+ *   prompt is cut (up to rounding), and Tq = 1 is a decode step.  With a window only the
+ *   rows that some query of the chunk sees are used.
  *   q, o bf16 [B, Hq, Tq, d]; k_new, v_new bf16 [B, Hkv, Tq, d], contiguous; lse fp32
  *   [B, Hq, Tq] (nullable); q must stay in the fp16 range as in yr_attn_prefill.
  *   workspace: 256-byte aligned; yr_attn_prefill_chunk_kv4_workspace_bytes() gives room
- *     for the fp16 rows and for the split-KV partials of a short chunk.  The former are
+ *     for the fp16 rows and for the split-KV partials of either kernel.  The former are
  *     needed -- yr_attn_prefill_workspace_bytes(B, Hkv, P0 + Tq, d) rounded up to 256 --
- *     less than the rest limits the split.
+ *     less than the rest limits the split, and may leave a few tokens to the prefill kernel.
  *
  * Errors: YR_EINVAL for NULL or misaligned pointers, sizes or flags out of range (B, Hkv
  *   <= 65535 for all but attn_decode_kv4; positions <= 2^30), Hq not a multiple of Hkv, a

@@ -467,6 +467,74 @@ def test_chunk_alibi():
     run_chunk(gen_of(2), 1, 8, 4, 128, 500, 99, 700, method="alibi")
 
 
+# A few tokens are taken by the decode kernel, tokens times heads as its columns.
+@pytest.mark.parametrize("Hq,Hkv,d,pairs", [(4, 4, 128, "half"), (8, 2, 128, "interleaved"),
+                                            (16, 2, 64, "half"), (16, 1, 128, "interleaved"),
+                                            (6, 2, 64, "interleaved"), (10, 2, 128, "half")])
+@pytest.mark.parametrize("Tq", [1, 2, 3, 7, 16, 17])
+def test_short_chunk_heads_and_tokens(Hq, Hkv, d, pairs, Tq):
+    run_chunk(gen_of(Hq + Tq), 2, Hq, Hkv, d, 777, Tq, 777 + Tq, pairs, poison=True)
+
+
+@pytest.mark.parametrize("P0", [0, 1, 30, 31, 32, 33, 127, 4000])
+def test_short_chunk_after_any_prefix(P0):
+    run_chunk(gen_of(P0), 1, 8, 2, 128, P0, 9, P0 + 11, poison=True)
+
+
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (3, 0), (5, 2), (40, 0), (64, 4), (300, 70),
+                                           (900, 500), (5000, 1)])
+@pytest.mark.parametrize("d,Tq", [(64, 10), (128, 5)])
+def test_short_chunk_window_and_sinks_use_only_what_is_seen(window, n_sink, d, Tq):
+    run_chunk(gen_of(window + d), 2, 8, 4, d, 1001, Tq, 1100, window=window, n_sink=n_sink,
+              poison=True)
+
+
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (100, 3)])
+def test_short_chunk_alibi(window, n_sink):
+    run_chunk(gen_of(3), 1, 12, 4, 128, 600, 6, 700, method="alibi", window=window, n_sink=n_sink)
+
+
+@pytest.mark.parametrize("window", [0, 200])
+def test_short_chunk_within_a_small_workspace(window):
+    """A workspace with room for the 16-bit rows alone takes the other kernel; both are right."""
+    gen, d, Hq, Hkv, P0, Tq = gen_of(23), 128, 8, 2, 600, 4
+    tab = table(d)
+    cache = random_rows(gen, 1, Hkv, P0 + Tq, d)
+    q = randn(gen, 1, Hq, Tq, d).bfloat16()
+    k, v = new_kv(gen, 1, Hkv, Tq, d)
+    planes = (api.attn_prefill_workspace_bytes(1, Hkv, P0 + Tq, d) + 255) // 256 * 256
+    full = api.attn_prefill_chunk_kv4_workspace_bytes(1, Hq, Hkv, Tq, d, P0)
+    assert planes < full
+    pos = P0 + torch.arange(Tq, device="cuda")
+    for n in (planes, full):
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        o = api.attn_prefill_chunk_kv4(q, k, v, cache, P0, tab, window, workspace=ws)
+        api.device_status()
+        rows = cache[0].clone()
+        if window:
+            rows[:, : P0 + 1 - window] = 0
+        ro, rl, amp, logit = R.attend(R.rotate(q[0], pos, tab), rows, pos, tab, window)
+        bo, _ = chunk_bounds(ro, rl, amp, logit)
+        assert ((o[0].double() - ro).abs() <= bo).all()
+
+
+def test_short_chunk_meets_the_decode_kernels_bounds():
+    """Its queries have 22 bits and its rows are taken exactly, as in a decode step."""
+    gen, d, Hq, Hkv, P0, Tq = gen_of(29), 128, 16, 4, 1500, 4
+    tab = table(d)
+    cache = random_rows(gen, 1, Hkv, P0 + Tq, d)
+    q = randn(gen, 1, Hq, Tq, d).bfloat16()
+    k, v = new_kv(gen, 1, Hkv, Tq, d)
+    lse = torch.empty(1, Hq, Tq, device="cuda")
+    o = api.attn_prefill_chunk_kv4(q, k, v, cache, P0, tab, lse=lse)
+    api.device_status()
+    pos = P0 + torch.arange(Tq, device="cuda")
+    ro, rl, amp, logit = R.attend(R.rotate(q[0], pos, tab), cache[0], pos, tab)
+    bo, bl = R.decode_bounds(ro, rl, amp, logit, P0 + Tq, d)
+    assert ((o[0].double() - ro).abs() <= bo).all()
+    assert ((lse[0].double() - rl).abs() <= bl).all()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_chunk_does_not_depend_on_where_a_prompt_is_cut(d):
     """One chunk, two chunks, and decode steps leave the same cache and agree."""

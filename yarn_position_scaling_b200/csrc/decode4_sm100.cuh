@@ -21,19 +21,22 @@ constexpr int kDec4Warps = 4;
 constexpr int kDec4Threads = kDec4Warps * 32;
 constexpr int kDec4Tile = 32;  // keys of one bulk copy
 constexpr int kDec4Stages = 2;
+constexpr float kNoScore = -1e30f;  // the reference of a column that has seen no key yet
 constexpr int kDec4Step = 32;  // keys that a warp takes through scores and outputs at a time
 
 struct Decode4Params {
-    const __nv_bfloat16 *q_new;          // [B][Hq][d]
-    const __nv_bfloat16 *k_new, *v_new;  // [B][Hkv][d]
+    const __nv_bfloat16 *q_new;          // [B][Hq][Tq][d]
+    const __nv_bfloat16 *k_new, *v_new;  // [B][Hkv][d], Tq = 1: the row to append; or null
     uint8_t *kv4;                        // [B][Hkv][T_max][5d/4]
-    const int *cache_len;                // [B]
-    float *ws_o;                         // [slots][g][d]
-    float *ws_ml;                        // [slots][g][2]
-    __nv_bfloat16 *o;                    // [B][Hq][d]
-    float *lse;                          // [B][Hq] or null
+    const int *cache_len;                // [B], position of the first token; or null: P0
+    float *ws_o;                         // [slots][seg_tokens g][d]
+    float *ws_ml;                        // [slots][seg_tokens g][2]
+    __nv_bfloat16 *o;                    // [B][Hq][Tq][d]
+    float *lse;                          // [B][Hq][Tq] or null
     __nv_bfloat16 *k_stored, *v_stored;  // [B][Hkv][d] or null
     int B, Hq, Hkv, T_max, group;
+    int P0, Tq;
+    int seg_tokens, n_segs;  // tokens of a segment, segments of a sequence and KV head
     int grid_blocks;
     int window, n_sink;
     float sl2;  // softmax scale times log2 e
@@ -42,21 +45,41 @@ struct Decode4Params {
     double turns[64];
 };
 
-// Ranges [0, len1) and [lo2, lo2 + len2) of keys that the token at position L sees.
-__device__ __forceinline__ DecRanges dec4_ranges(const Decode4Params &p, int L) {
-    DecRanges r{0, 0, 0};
-    if (L < 0 || L > p.T_max - 1) return r;
-    const int s1 = min(p.n_sink, L + 1);
-    const int w0 = p.window > 0 ? max(L - p.window + 1, 0) : 0;
+// Segment st of the B n_segs (sequence, run of tokens) pairs: positions first .. last of its
+// tokens, and the ranges [0, len1) and [lo2, lo2 + len2) of the keys that one of them sees.
+struct Dec4Seg {
+    int first, last;
+    DecRanges keys;
+};
+// (kMulti: more than one token; a decode step's code is spared the divisions and masks.)
+template <bool kMulti>
+__device__ __forceinline__ int dec4_sequence(const Decode4Params &p, int st) {
+    return kMulti ? st / p.n_segs : st;
+}
+// Token of a column within its segment.
+template <bool kMulti>
+__device__ __forceinline__ int dec4_token(const Decode4Params &p, int col) {
+    return kMulti ? col / p.group : 0;
+}
+template <bool kMulti>
+__device__ __forceinline__ Dec4Seg dec4_seg(const Decode4Params &p, int st) {
+    Dec4Seg s{0, -1, {0, 0, 0}};
+    const int b = dec4_sequence<kMulti>(p, st), t0 = kMulti ? (st - b * p.n_segs) * p.seg_tokens : 0;
+    const int L = kMulti ? p.P0 : p.cache_len[b];
+    if (L < 0 || L > p.T_max - (kMulti ? p.Tq : 1)) return s;
+    s.first = L + t0;
+    s.last = kMulti ? L + min(t0 + p.seg_tokens, p.Tq) - 1 : L;
+    const int s1 = min(p.n_sink, s.last + 1);
+    const int w0 = p.window > 0 ? max(s.first - p.window + 1, 0) : 0;
     if (w0 <= s1) {
-        r.len1 = L + 1;
-        r.lo2 = L + 1;
+        s.keys.len1 = s.last + 1;
+        s.keys.lo2 = s.last + 1;
     } else {
-        r.len1 = s1;
-        r.lo2 = w0;
-        r.len2 = L + 1 - w0;
+        s.keys.len1 = s1;
+        s.keys.lo2 = w0;
+        s.keys.len2 = s.last + 1 - w0;
     }
-    return r;
+    return s;
 }
 
 // The partition, as every block derives it from cache_len.  A segment is `lead` units for
@@ -67,8 +90,9 @@ struct Dec4Plan {
     long long U;  // units of a block
     int lead;
 };
-__device__ __forceinline__ int dec4_keys(const Decode4Params &p, int b) {
-    const DecRanges r = dec4_ranges(p, p.cache_len[b]);
+template <bool kMulti>
+__device__ __forceinline__ int dec4_keys(const Decode4Params &p, int st) {
+    const DecRanges r = dec4_seg<kMulti>(p, st).keys;
     return r.len1 + r.len2;
 }
 // Units of a segment: none for a length outside the cache.
@@ -76,11 +100,12 @@ __device__ __forceinline__ long long dec4_units(int keys, int lead) {
     return keys > 0 ? static_cast<long long>(keys) + lead : 0;
 }
 // Called by a full warp.
+template <bool kMulti>
 __device__ __forceinline__ Dec4Plan dec4_plan(const Decode4Params &p, int lane) {
     long long keys = 0;
     int segs = 0;
-    for (int b = lane; b < p.B; b += 32) {
-        const int n = dec4_keys(p, b);
+    for (int st = lane; st < (kMulti ? p.B * p.n_segs : p.B); st += 32) {
+        const int n = dec4_keys<kMulti>(p, st);
         keys += n;
         segs += n > 0;
     }
@@ -192,7 +217,7 @@ struct Decode4Smem {
     alignas(128) uint8_t ring[kDec4Warps][kDec4Stages][kStageBytes];  // also the warps' outputs
     alignas(16) uint8_t new_row[kv4_row_bytes(HD)];
     double2 cs[HD / 2];
-    float2 q_cs[HD / 2];
+    float2 q_cs[8 * NT][HD / 2];  // by token
     uint4 q_hi[8 * NT][HD / 8], q_lo[8 * NT][HD / 8];  // fragments, see the rotation below
     float q_sum[8 * NT][HD / kKv4Group];  // sums of the scaled query over the groups
     float q_scale[8 * NT];  // what takes the scaled query back
@@ -223,7 +248,7 @@ constexpr size_t decode4_smem_bytes() {
 //   p z in fp32.  p = 2^(score - R) for a reference R per head that puts the largest p s of
 //   a tile at 2^8 and is raised only once one passes 2^15: small scales keep their bits
 //   (fp16 holds 2^-14 at full precision), and the common tile costs one vote.
-template <int HD, int NT, int REP, bool kHalf>
+template <int HD, int NT, int REP, bool kHalf, bool kMulti>
 __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     decode4_split_kernel(const __grid_constant__ Decode4Params p) {
     using Smem = Decode4Smem<HD, NT>;
@@ -243,22 +268,23 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     const int val_at0 = dec4_key<HD>(2 * r) * kRow + HD / 2 + (G == 4 ? 8 : 4) * c;
     const int val_at1 = dec4_key<HD>(2 * r + 1) * kRow + HD / 2 + (G == 4 ? 8 : 4) * c;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Dec4Plan plan = dec4_plan(p, lane);
+    const Dec4Plan plan = dec4_plan<kMulti>(p, lane);
     const long long u_lo = blockIdx.x * plan.U, u_hi = u_lo + plan.U;
-    if (blockIdx.x == 0 && tid == 0)
-        for (int b = 0; b < p.B; ++b)
+    if (!kMulti && blockIdx.x == 0)
+        for (int b = tid; b < p.B; b += kDec4Threads)
             if (p.cache_len[b] < 0 || p.cache_len[b] > p.T_max - 1) raise_status(kStatusBadCacheLen);
     // This warp's ring, over all segments: the stages of the next copy and the next wait,
     // and the parity of the latter.
     uint32_t s_load = 0, s_wait = 0, parity = 0;
     const uint64_t policy = l2_policy_evict_first();
 
-    // Sequences before the first one of this block.
-    int b = 0;
+    // Segments before the first one of this block.
+    int st = 0;
     long long seg0 = 0;
-    for (long long v; b < p.B && seg0 + (v = p.Hkv * dec4_units(dec4_keys(p, b), plan.lead)) <= u_lo; ++b)
+    const int n_st = kMulti ? p.B * p.n_segs : p.B;
+    for (long long v; st < n_st && seg0 + (v = p.Hkv * dec4_units(dec4_keys<kMulti>(p, st), plan.lead)) <= u_lo; ++st)
         seg0 += v;
-    if (b == p.B) return;
+    if (st == n_st) return;
     if (tid == 0) {
         for (int w = 0; w < kDec4Warps; ++w)
             for (int s = 0; s < kDec4Stages; ++s) mbar_init(&sm->full[w][s], 1);
@@ -266,9 +292,12 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
         fence_mbar_init();
     }
     __syncthreads();
-    for (; b < p.B && seg0 < u_hi; ++b) {
-        const int L = p.cache_len[b];
-        const DecRanges rg = dec4_ranges(p, L);
+    for (; st < n_st && seg0 < u_hi; ++st) {
+        const Dec4Seg seg = dec4_seg<kMulti>(p, st);
+        const DecRanges rg = seg.keys;
+        const int L = seg.last, b = dec4_sequence<kMulti>(p, st);
+        const int t0 = kMulti ? (st - b * p.n_segs) * p.seg_tokens : 0, n_tok = kMulti ? seg.last - seg.first + 1 : 1;
+        const int cols = n_tok * g;  // column: token times heads plus head
         const long long V = dec4_units(rg.len1 + rg.len2, plan.lead);
         if (V == 0) continue;
         int kvh = seg0 < u_lo ? static_cast<int>((u_lo - seg0) / V) : 0;
@@ -284,8 +313,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
             const int lo2 = rg.lo2 + max(u0, rg.len1) - rg.len1;
             const int hi2 = rg.lo2 + max(u1, rg.len1) - rg.len1;
             const int n_t1 = (hi1 - lo1 + kDec4Tile - 1) / kDec4Tile;
-            // The new row is the last of the last block's keys: of the range that ends there.
-            const bool has_L = u1 == rg.len1 + rg.len2;
+            // A row to append is the last of the last block's keys.
+            const bool has_L = !kMulti && u1 == rg.len1 + rg.len2;
             uint8_t *plane = p.kv4 + (static_cast<long long>(b) * p.Hkv + kvh) * p.T_max * kRow;
             // This warp's tiles, as copies and as steps pass through them: every fourth of the
             // first range, then of the second, the warps taking turns across the seam.
@@ -307,7 +336,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
             auto load = [&] {  // the cached rows of the next tile: all but the new one
                 if (lane == 0) {
                     const int n = min(kDec4Tile, ld_end - ld_key);
-                    const uint32_t bytes = (n - (ld_key + n > L ? 1 : 0)) * kRow;
+                    const uint32_t bytes = (n - (has_L && ld_key + n > L ? 1 : 0)) * kRow;
                     uint64_t *bar = &sm->full[warp][s_load];
                     mbar_arrive_expect_tx(bar, bytes);
                     if (bytes > 0)
@@ -329,24 +358,25 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
             for (int n = 0; n < kPer; ++n) {
                 const int i = tid + n * kDec4Threads, h = i / (HD / 8), ch = i % (HD / 8);
                 raw[n] = other[n] = make_uint4(0, 0, 0, 0);
-                if (i < kItems && h < g) {
+                if (i < kItems && h < cols) {
                     const uint4 *row = reinterpret_cast<const uint4 *>(
-                        p.q_new + (static_cast<long long>(b) * p.Hq + kvh * g + h) * HD);
+                        p.q_new + ((static_cast<long long>(b) * p.Hq + kvh * g + h - dec4_token<kMulti>(p, h) * g) * (kMulti ? p.Tq : 1) + t0 + dec4_token<kMulti>(p, h)) * HD);
                     raw[n] = __ldg(row + ch);
                     if (kHalf) other[n] = __ldg(row + (ch ^ (HD / 16)));
                 }
             }
             // The new row wants its sines in 64 bits; the queries' 22 bits do with fp32 ones.
-            for (int i = tid; i < HD / 2; i += kDec4Threads) {
+            for (int n = tid; n < n_tok * (HD / 2); n += kDec4Threads) {
+                const int i = n % (HD / 2), tok = n / (HD / 2);
                 if (has_L) {
                     const double2 t = kv4_cos_sin(L, p.turns[i]);
                     sm->cs[i] = t;
-                    sm->q_cs[i] = make_float2(static_cast<float>(t.x), static_cast<float>(t.y));
+                    sm->q_cs[0][i] = make_float2(static_cast<float>(t.x), static_cast<float>(t.y));
                 } else {
-                    const double tr = static_cast<double>(L) * p.turns[i];
+                    const double tr = static_cast<double>(seg.first + tok) * p.turns[i];
                     float sn, co;
                     sincospif(2.f * static_cast<float>(tr - rint(tr)), &sn, &co);
-                    sm->q_cs[i] = make_float2(co, sn);
+                    sm->q_cs[tok][i] = make_float2(co, sn);
                 }
             }
             __syncthreads();
@@ -356,19 +386,20 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 if (i >= kItems) break;
                 float x[8], y[8], mx = 0.f;
                 unpack_bf16x8(raw[n], x);
+                const float2 *cs = sm->q_cs[h < cols ? dec4_token<kMulti>(p, h) : 0];
                 if constexpr (kHalf) {
                     float z[8];
                     unpack_bf16x8(other[n], z);
                     const int c0 = 8 * (ch % (HD / 16));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float2 t = sm->q_cs[c0 + e];
+                        const float2 t = cs[c0 + e];
                         y[e] = ch < HD / 16 ? x[e] * t.x - z[e] * t.y : z[e] * t.y + x[e] * t.x;
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 t = sm->q_cs[4 * ch + e];
+                        const float2 t = cs[4 * ch + e];
                         y[2 * e] = x[2 * e] * t.x - x[2 * e + 1] * t.y;
                         y[2 * e + 1] = x[2 * e] * t.y + x[2 * e + 1] * t.x;
                     }
@@ -403,7 +434,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 if (ch == 0) {
                     sm->q_scale[h] = pow2i(e2 - 7);
                     // ALiBi's slope in units of a score before its scaling by sl2 q_scale.
-                    sm->slope[h] = p.alibi ? exp2f(-8.0f * static_cast<float>(kvh * g + h + 1) /
+                    sm->slope[h] = p.alibi ? exp2f(-8.0f * static_cast<float>(kvh * g + h - dec4_token<kMulti>(p, h) * g + 1) /
                                                    static_cast<float>(p.Hq)) * 1.4426950408889634f /
                                                  (p.sl2 * pow2i(e2 - 7))
                                            : 0.f;
@@ -451,7 +482,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    R[nt][j] = -INFINITY;
+                    R[nt][j] = kNoScore;
                     l[nt][j] = 0.f;
 #pragma unroll
                     for (int k = 0; k < GL; ++k) w[nt][j][k] = 0.f;
@@ -487,7 +518,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                     parity ^= 1;
                 }
                 const int n_keys = min(kDec4Tile, end - key);
-                if (key + n_keys > L) {  // the tile of the new row
+                if (has_L && key + n_keys > L) {  // the tile of the new row
                     if (lane < kRow / 16)
                         reinterpret_cast<uint4 *>(const_cast<uint8_t *>(ring) + (n_keys - 1) * kRow)[lane] =
                             reinterpret_cast<const uint4 *>(sm->new_row)[lane];
@@ -580,25 +611,37 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const float slope = sm->slope[nt * 8 + 2 * (r % kCopy) + j];
+                            const int col = nt * 8 + 2 * (r % kCopy) + j, pos = seg.first + dec4_token<kMulti>(p, col);
+                            const float slope = sm->slope[col];
 #pragma unroll
                             for (int t = 0; t < H; ++t)
 #pragma unroll
                                 for (int k = 0; k < 2; ++k)
-                                    x[t][nt][2 * k + j] = fmaf(-slope, static_cast<float>(L - key - (k0 + 16 * t + 8 * k + dec4_key<HD>(c))), x[t][nt][2 * k + j]);
+                                    x[t][nt][2 * k + j] = fmaf(-slope, static_cast<float>(pos - key - (k0 + 16 * t + 8 * k + dec4_key<HD>(c))), x[t][nt][2 * k + j]);
                         }
                 }
-                if (n_keys < kDec4Tile) {  // rows behind the tile's end do not count
+                // Rows behind the tile's end do not count, nor keys that a column does not see.
+                if (n_keys < kDec4Tile || (kMulti && (key + kDec4Tile - 1 > seg.first ||
+                                              (p.window > 0 && key <= seg.last - p.window && key + kDec4Tile > p.n_sink)))) {
 #pragma unroll
                     for (int t = 0; t < H; ++t)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (k0 + 16 * t + 8 * k + dec4_key<HD>(c) >= n_keys) {
+                        for (int k = 0; k < 2; ++k) {
+                            const int i = k0 + 16 * t + 8 * k + dec4_key<HD>(c), n = key + i;
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) x[t][nt][2 * k] = x[t][nt][2 * k + 1] = -INFINITY;
+                            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int i = 0; i < GL; ++i) par[t][k][i] = 0;
+                                for (int j = 0; j < 2; ++j) {
+                                    const int pos = seg.first + dec4_token<kMulti>(p, nt * 8 + 2 * (r % kCopy) + j);
+                                    if (i >= n_keys ||
+                                        (kMulti && (n > pos || (p.window > 0 && n <= pos - p.window && n >= p.n_sink))))
+                                        x[t][nt][2 * k + j] = -INFINITY;
+                                }
+                            if (i >= n_keys) {
+#pragma unroll
+                                for (int m = 0; m < GL; ++m) par[t][k][m] = 0;
                             }
+                        }
                 }
                 // Probabilities and B operands; true if one of the latter nears fp16's end (or
                 // would, but for a scale of 0).
@@ -661,8 +704,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                                 t = fmaxf(t, fmaf(x[k >> 1][nt][2 * (k & 1) + j], x_scale[nt][j], ls[k >> 1][k & 1]));
 #pragma unroll
                             for (int off = kCopy; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-                            if (!(fabsf(t) < INFINITY)) t = R[nt][j] == -INFINITY ? 0.f : R[nt][j];
-                            const float f = R[nt][j] == -INFINITY ? 0.f : ex2f(R[nt][j] - t);
+                            if (!(fabsf(t) < INFINITY)) t = R[nt][j];
+                            const float f = R[nt][j] == kNoScore ? 0.f : ex2f(R[nt][j] - t);
                             R[nt][j] = t;
                             l[nt][j] *= f;
 #pragma unroll
@@ -738,7 +781,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                             w[nt][j][i] += __shfl_xor_sync(0xffffffffu, w[nt][j][i], off);
                     }
                     if (lane < kCopy) {
-                        sm->m[warp][nt * 8 + 2 * r + j] = R[nt][j];
+                        sm->m[warp][nt * 8 + 2 * r + j] = l[nt][j] == 0.f ? -INFINITY : R[nt][j];
                         sm->l[warp][nt * 8 + 2 * r + j] = l[nt][j];
                     }
                 }
@@ -761,8 +804,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                     }
             }
             __syncthreads();
-            const long long slot = (blockIdx.x + static_cast<long long>(b) * p.Hkv + kvh) * g;
-            for (int i = tid; i < g * HD; i += kDec4Threads) {
+            const long long slot = (blockIdx.x + static_cast<long long>(st) * p.Hkv + kvh) * (kMulti ? p.seg_tokens * g : g);
+            for (int i = tid; i < cols * HD; i += kDec4Threads) {
                 const int h = i / HD, dim = i % HD;
                 float top_m = -INFINITY, acc = 0.f, sum = 0.f;
 #pragma unroll
@@ -785,41 +828,43 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     }
 }
 
-// One block per (query head, sequence): the pieces of its segment, by log-sum-exp weights.
+// One block per (sequence, query head, token): the pieces of its segment, by log-sum-exp weights.
 // Four warps share the pieces, a lane holding HD/32 dims, so that few loads follow one another
 // (one warp's turn through 40 pieces took 8 us, this 3).
 constexpr int kDec4MergeThreads = 128;
-template <int HD>
+template <int HD, bool kMulti>
 __global__ void __launch_bounds__(kDec4MergeThreads) decode4_merge_kernel(const __grid_constant__ Decode4Params p) {
     constexpr int kVec = HD / 32, kWarps = kDec4MergeThreads / 32;
     __shared__ float weight[kDec4MaxBlocks];
     __shared__ float red[kWarps], out[kWarps][HD];
-    const int hq = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
+    const int oi = blockIdx.x, Tq = kMulti ? p.Tq : 1, t = oi % Tq, hq = oi / Tq % p.Hq, b = oi / Tq / p.Hq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int L = p.cache_len[b], g = p.group, kvh = hq / g, hh = hq % g;
-    const long long oi = static_cast<long long>(b) * p.Hq + hq;
-    const DecRanges rg = dec4_ranges(p, L);
-    if (rg.len1 + rg.len2 == 0) {  // a length outside the cache
+    const int g = p.group, kvh = hq / g;
+    const int st = kMulti ? b * p.n_segs + t / p.seg_tokens : b;
+    const int col = (kMulti ? t % p.seg_tokens * g : 0) + hq % g;
+    const int keys = dec4_keys<kMulti>(p, st);
+    if (keys == 0) {  // a length outside the cache
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (tid < HD) p.o[oi * HD + tid] = __float2bfloat16(__int_as_float(0x7fc00000));
+        if (tid < HD) p.o[static_cast<long long>(oi) * HD + tid] = __float2bfloat16(__int_as_float(0x7fc00000));
         if (p.lse != nullptr && tid == 0) p.lse[oi] = __int_as_float(0x7fc00000);
         return;
     }
-    const Dec4Plan plan = dec4_plan(p, lane);
+    const Dec4Plan plan = dec4_plan<kMulti>(p, lane);
     long long seg0 = 0;
-    for (int i = lane; i < b; i += 32) seg0 += p.Hkv * dec4_units(dec4_keys(p, i), plan.lead);
+    for (int i = lane; i < st; i += 32) seg0 += p.Hkv * dec4_units(dec4_keys<kMulti>(p, i), plan.lead);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) seg0 += __shfl_xor_sync(0xffffffffu, seg0, off);
-    const long long V = dec4_units(rg.len1 + rg.len2, plan.lead);
+    const long long V = dec4_units(keys, plan.lead);
     seg0 += kvh * V;
     const int first = static_cast<int>((seg0 + plan.lead) / plan.U);
     const int n = static_cast<int>((seg0 + V - 1) / plan.U) - first + 1;  // pieces, at most one a block
-    const long long slot0 = (first + static_cast<long long>(b) * p.Hkv + kvh) * g + hh;
+    const int rows = kMulti ? p.seg_tokens * g : g;
+    const long long slot0 = (first + static_cast<long long>(st) * p.Hkv + kvh) * rows + col;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's results
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
     float M = -INFINITY, sum = 0.f;
     for (int i = tid; i < n; i += kDec4MergeThreads) {
-        weight[i] = ml[slot0 + static_cast<long long>(i) * g].x;
+        weight[i] = ml[slot0 + static_cast<long long>(i) * rows].x;
         M = fmaxf(M, weight[i]);
     }
 #pragma unroll
@@ -833,7 +878,7 @@ __global__ void __launch_bounds__(kDec4MergeThreads) decode4_merge_kernel(const 
     for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
 #pragma unroll 4
     for (int i = warp; i < n; i += kWarps) {
-        const long long s = slot0 + static_cast<long long>(i) * g;
+        const long long s = slot0 + static_cast<long long>(i) * rows;
         const float w = M == -INFINITY ? 0.f : ex2f(weight[i] - M);
         const float *o = p.ws_o + s * HD + kVec * lane;
         sum = fmaf(w, ml[s].y, sum);
@@ -861,7 +906,7 @@ __global__ void __launch_bounds__(kDec4MergeThreads) decode4_merge_kernel(const 
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += out[w][tid];
-        p.o[oi * HD + tid] = __float2bfloat16_rn(v / sum);
+        p.o[static_cast<long long>(oi) * HD + tid] = __float2bfloat16_rn(v / sum);
     }
     if (p.lse != nullptr && tid == 0) p.lse[oi] = (M + log2f(sum)) * 0.69314718055994531f;
 }

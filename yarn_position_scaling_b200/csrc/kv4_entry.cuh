@@ -90,18 +90,34 @@ int launch_kv4_read(yr::Kv4ReadParams rp, int d, bool f16, int sm_count, cudaStr
     return YR_OK;
 }
 
+// Workspace of the split kernel: a slot per block and per segment of `rows` rows each.
+size_t decode4_slots_bytes(long long segments, long long rows, long long d) {
+    return static_cast<size_t>((yr::kDec4MaxBlocks + segments) * rows * (d + 2) * 4);
+}
 size_t decode4_ws_bytes(long long B, long long Hq, long long Hkv, long long d) {
-    return static_cast<size_t>((yr::kDec4MaxBlocks + B * Hkv) * (Hq / Hkv) * (d + 2) * 4);
+    return decode4_slots_bytes(B * Hkv, Hq / Hkv, d);
+}
+
+// A chunk's tokens in runs that the split kernel takes as its columns (16, or 8 where all fit).
+struct Decode4Runs {
+    int tokens, n;
+};
+Decode4Runs decode4_runs(int g, int Tq) {
+    const int cols = Tq * g <= 8 ? 8 : 16;
+    int tokens = cols / g < Tq ? cols / g : Tq;
+    if (tokens < 1) tokens = 1;
+    tokens = (Tq + (Tq + tokens - 1) / tokens - 1) / ((Tq + tokens - 1) / tokens);  // evenly
+    return {tokens, (Tq + tokens - 1) / tokens};
 }
 
 // One wave of the split kernel, and the places of its partial results.
-template <int HD, int NT, int REP, bool kHalf>
+template <int HD, int NT, int REP, bool kHalf, bool kMulti>
 int launch_decode4_form(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
     static int per_sm = 0;  // same value on every device of this build's target
     if (per_sm == 0) {
         int n = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &n, yr::decode4_split_kernel<HD, NT, REP, kHalf>, yr::kDec4Threads,
+                &n, yr::decode4_split_kernel<HD, NT, REP, kHalf, kMulti>, yr::kDec4Threads,
                 yr::decode4_smem_bytes<HD, NT>()) != cudaSuccess ||
             n < 1)
             n = 1;
@@ -109,23 +125,55 @@ int launch_decode4_form(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
     }
     const int blocks = per_sm * sm_count;
     dp.grid_blocks = blocks < yr::kDec4MaxBlocks ? blocks : yr::kDec4MaxBlocks;
-    const long long slots = dp.grid_blocks + static_cast<long long>(dp.B) * dp.Hkv;
-    dp.ws_ml = dp.ws_o + slots * dp.group * HD;
-    yr::decode4_split_kernel<HD, NT, REP, kHalf>
+    const long long slots = dp.grid_blocks + static_cast<long long>(dp.B) * dp.n_segs * dp.Hkv;
+    dp.ws_ml = dp.ws_o + slots * dp.seg_tokens * dp.group * HD;
+    yr::decode4_split_kernel<HD, NT, REP, kHalf, kMulti>
         <<<dp.grid_blocks, yr::kDec4Threads, yr::decode4_smem_bytes<HD, NT>(), st>>>(dp);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("decode4_split_kernel launch", e);
     return YR_OK;
 }
 
-// The form of the kernel for g query heads per KV head.
-template <int HD, bool kHalf>
+// The form of the kernel for a segment's columns (tokens times query heads per KV head).
+template <int HD, bool kHalf, bool kMulti>
 int launch_decode4(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
-    const int g = dp.group;
-    if (g > 8) return launch_decode4_form<HD, 2, 1, kHalf>(dp, sm_count, st);
-    if (g > 4) return launch_decode4_form<HD, 1, 1, kHalf>(dp, sm_count, st);
-    if (g > 2 || HD == 64) return launch_decode4_form<HD, 1, 2, kHalf>(dp, sm_count, st);
-    return launch_decode4_form<HD, 1, HD / 32, kHalf>(dp, sm_count, st);
+    const int cols = dp.seg_tokens * dp.group;
+    if (cols > 8) return launch_decode4_form<HD, 2, 1, kHalf, kMulti>(dp, sm_count, st);
+    if (cols > 4) return launch_decode4_form<HD, 1, 1, kHalf, kMulti>(dp, sm_count, st);
+    if (cols > 2 || HD == 64) return launch_decode4_form<HD, 1, 2, kHalf, kMulti>(dp, sm_count, st);
+    return launch_decode4_form<HD, 1, HD / 32, kHalf, kMulti>(dp, sm_count, st);
+}
+
+// The split kernel over dp's segments and the merge of its partial results.
+template <bool kMulti>
+int launch_decode4_call(yr::Decode4Params &dp, int d, const yr_rope_table *tab, int sm_count,
+                        cudaStream_t st) {
+    dp.sl2 = static_cast<float>(tab->softmax_scale * 1.4426950408889634);
+    dp.alibi = tab->method == YR_ALIBI ? 1 : 0;
+    for (int i = 0; i < d / 2; ++i) dp.turns[i] = tab->turns[i];
+    dp.timeout_ns = wait_timeout_ns();
+    const bool half = tab->pairs == YR_PAIR_HALF;
+    int rc = d == 128 ? half ? launch_decode4<128, true, kMulti>(dp, sm_count, st)
+                         : launch_decode4<128, false, kMulti>(dp, sm_count, st)
+         : half   ? launch_decode4<64, true, kMulti>(dp, sm_count, st)
+                  : launch_decode4<64, false, kMulti>(dp, sm_count, st);
+    if (rc != YR_OK) return rc;
+    // The merge may start, and find its pieces, while the split kernel still runs; it waits
+    // for that kernel's results itself.
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(dp.B) * dp.Hq * dp.Tq);
+    cfg.blockDim = dim3(yr::kDec4MergeThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = d == 128 ? cudaLaunchKernelEx(&cfg, yr::decode4_merge_kernel<128, kMulti>, dp)
+                                   : cudaLaunchKernelEx(&cfg, yr::decode4_merge_kernel<64, kMulti>, dp);
+    if (e != cudaSuccess) return cuda_fail("decode4_merge_kernel launch", e);
+    return YR_OK;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -252,42 +300,44 @@ extern "C" int yr_attn_decode_kv4(const void *q_new, const void *k_new, const vo
     dp.v_stored = static_cast<__nv_bfloat16 *>(v_stored);
     dp.B = B; dp.Hq = Hq; dp.Hkv = Hkv; dp.T_max = T_max; dp.group = g;
     dp.window = window; dp.n_sink = n_sink;
-    dp.sl2 = static_cast<float>(tab->softmax_scale * 1.4426950408889634);
-    dp.alibi = tab->method == YR_ALIBI ? 1 : 0;
-    for (int i = 0; i < d / 2; ++i) dp.turns[i] = tab->turns[i];
-    dp.timeout_ns = wait_timeout_ns();
+    dp.Tq = 1; dp.seg_tokens = 1; dp.n_segs = 1;
     dp.ws_o = static_cast<float *>(workspace);
-    const bool half = tab->pairs == YR_PAIR_HALF;
-    rc = d == 128 ? half ? launch_decode4<128, true>(dp, sm_count, st)
-                         : launch_decode4<128, false>(dp, sm_count, st)
-         : half   ? launch_decode4<64, true>(dp, sm_count, st)
-                  : launch_decode4<64, false>(dp, sm_count, st);
-    if (rc != YR_OK) return rc;
-    // The merge may start, and find its pieces, while the split kernel still runs; it waits
-    // for that kernel's results itself.
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(static_cast<unsigned>(B) * Hq);
-    cfg.blockDim = dim3(yr::kDec4MergeThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = d == 128 ? cudaLaunchKernelEx(&cfg, yr::decode4_merge_kernel<128>, dp)
-                                   : cudaLaunchKernelEx(&cfg, yr::decode4_merge_kernel<64>, dp);
-    if (e != cudaSuccess) return cuda_fail("decode4_merge_kernel launch", e);
-    return YR_OK;
+    return launch_decode4_call<false>(dp, d, tab, sm_count, st);
 }
+
+namespace yr_host {
+
+// Is a chunk of Tq tokens taken by the decode kernel, over the 4-bit rows, instead of by the
+// prefill kernel, over 16-bit copies of them?  The former reads the rows once for every 16
+// columns (tokens times query heads of a KV head), 60 ps a row (d = 128); the latter makes the
+// copies (110 ps a row) and then holds 256 query rows a tile, with a window 128, however few
+// there are (95 ps a row and query head, with a window half).  Both sides measured after 120K
+// keys of 8 KV heads, 32 query heads: 4 tokens 77 and 464 us, 16 tokens 245 and 465, 32 tokens
+// 469 and 467; with 64 query heads 16 tokens 470 and 809, 32 tokens 922 and 809.
+bool chunk4_by_decode(int g, int Tq, int window) {
+    if (g > 16) return false;
+    const int passes = decode4_runs(g, Tq).n;
+    return window > 0 ? passes <= 1 + g : 10 * passes <= 17 + 16 * g;
+}
+
+// Bytes that the decode kernel's partial results take for a chunk.
+size_t chunk4_decode_bytes(int B, int Hq, int Hkv, int Tq, int d) {
+    const Decode4Runs runs = decode4_runs(Hq / Hkv, Tq);
+    return decode4_slots_bytes(static_cast<long long>(B) * Hkv * runs.n,
+                               static_cast<long long>(runs.tokens) * (Hq / Hkv), d);
+}
+
+}  // namespace yr_host
 
 extern "C" size_t yr_attn_prefill_chunk_kv4_workspace_bytes(int B, int Hq, int Hkv, int Tq, int d,
                                                             int P0) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 1 || P0 < 0 || Hq % Hkv || (d != 64 && d != 128) ||
         static_cast<long long>(P0) + Tq > kKv4MaxPos)
         return 0;
-    return round256(prefill_ws_bytes(B, Hkv, static_cast<long long>(P0) + Tq, d)) +
-           kMaxSplit * split_share_bytes(B, Hq, Tq, d);
+    const size_t prefill = round256(prefill_ws_bytes(B, Hkv, static_cast<long long>(P0) + Tq, d)) +
+                           kMaxSplit * split_share_bytes(B, Hq, Tq, d);
+    const size_t decode = Hq / Hkv <= 16 ? chunk4_decode_bytes(B, Hq, Hkv, Tq, d) : 0;
+    return prefill > decode ? prefill : decode;
 }
 
 extern "C" int yr_attn_prefill_chunk_kv4(const void *q, const void *k_new, const void *v_new,
@@ -321,6 +371,21 @@ extern "C" int yr_attn_prefill_chunk_kv4(const void *q, const void *k_new, const
     rc = launch_kv4_write(k_new, v_new, kv4, B, Hkv, Tq, d, T_max, ks, ks, P0, nullptr, nullptr,
                           tab, sm_count, st);
     if (rc != YR_OK) return rc;
+    if (chunk4_by_decode(Hq / Hkv, Tq, window) &&
+        workspace_bytes >= chunk4_decode_bytes(B, Hq, Hkv, Tq, d)) {
+        const Decode4Runs runs = decode4_runs(Hq / Hkv, Tq);
+        yr::Decode4Params dp;
+        std::memset(&dp, 0, sizeof dp);
+        dp.q_new = static_cast<const __nv_bfloat16 *>(q);
+        dp.kv4 = static_cast<uint8_t *>(kv4);
+        dp.o = static_cast<__nv_bfloat16 *>(o);
+        dp.lse = lse;
+        dp.B = B; dp.Hq = Hq; dp.Hkv = Hkv; dp.T_max = T_max; dp.group = Hq / Hkv;
+        dp.P0 = P0; dp.Tq = Tq; dp.seg_tokens = runs.tokens; dp.n_segs = runs.n;
+        dp.window = window; dp.n_sink = n_sink;
+        dp.ws_o = static_cast<float *>(workspace);
+        return launch_decode4_call<true>(dp, d, tab, sm_count, st);
+    }
     // The rows in 16 bits for the attention: with a window, the 128-key tiles that it reads
     // and no others (those of the sinks, and from the first query's window on).
     const KvPlanes kv = workspace_planes(workspace, B, Hkv, Tk, d);

@@ -152,14 +152,18 @@ int prepare_device(int *sm_count, DeviceState *out = nullptr) {
                  yr::decode_smem_bytes<64>()},
                 {reinterpret_cast<const void *>(&yr::decode_split_kernel<64, 2>),
                  yr::decode_smem_bytes<64>()},
-#define YR_DECODE4(HD, NT, REP)                                                        \
-    {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, false>),    \
-     yr::decode4_smem_bytes<HD, NT>()},                                                \
-        {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, true>), \
+#define YR_DECODE4(HD, NT, REP, kHalf)                                                     \
+    {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, kHalf, false>), \
+     yr::decode4_smem_bytes<HD, NT>()},                                                    \
+        {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, kHalf, true>), \
          yr::decode4_smem_bytes<HD, NT>()}
-                YR_DECODE4(128, 1, 4), YR_DECODE4(128, 1, 2), YR_DECODE4(128, 1, 1),
-                YR_DECODE4(128, 2, 1), YR_DECODE4(64, 1, 2), YR_DECODE4(64, 1, 1),
-                YR_DECODE4(64, 2, 1),
+                YR_DECODE4(128, 1, 4, false), YR_DECODE4(128, 1, 4, true),
+                YR_DECODE4(128, 1, 2, false), YR_DECODE4(128, 1, 2, true),
+                YR_DECODE4(128, 1, 1, false), YR_DECODE4(128, 1, 1, true),
+                YR_DECODE4(128, 2, 1, false), YR_DECODE4(128, 2, 1, true),
+                YR_DECODE4(64, 1, 2, false), YR_DECODE4(64, 1, 2, true),
+                YR_DECODE4(64, 1, 1, false), YR_DECODE4(64, 1, 1, true),
+                YR_DECODE4(64, 2, 1, false), YR_DECODE4(64, 2, 1, true),
 #undef YR_DECODE4
             };
             for (auto &a : attrs) {
