@@ -15,7 +15,7 @@
 namespace yr {
 
 constexpr int kDec4Chunk = 128;      // least keys per block: a tile for each warp
-constexpr int kDec4Lead = 256;       // what a segment costs besides its keys, in keys
+constexpr int kDec4Lead = 256;       // what a segment costs besides its keys, in keys (4 us)
 constexpr int kDec4MaxBlocks = 640;  // most blocks of the split launch
 constexpr int kDec4Warps = 4;
 constexpr int kDec4Threads = kDec4Warps * 32;
@@ -82,45 +82,29 @@ __device__ __forceinline__ Dec4Seg dec4_seg(const Decode4Params &p, int st) {
     return s;
 }
 
-// The partition, as every block derives it from cache_len.  A segment is `lead` units for
-// what a block does once for it (query, partial result) and one for each key, so that blocks
-// of many short segments and blocks of few long ones take equally long; where there are
-// few keys for the blocks it is 0, and each takes as few keys as it may.
-struct Dec4Plan {
-    long long U;  // units of a block
-    int lead;
-};
+// The partition, as every block derives it from cache_len.  A segment is kDec4Lead units for
+// what a block does once for it (query, partial result) and one for each key: blocks of many
+// short segments and blocks of few long ones take equally long, and while there are blocks
+// enough no two segments' keys fall to the same one.  (Without the lead 88 segments of two keys
+// all went to one block and took 490 us.)
 template <bool kMulti>
 __device__ __forceinline__ int dec4_keys(const Decode4Params &p, int st) {
     const DecRanges r = dec4_seg<kMulti>(p, st).keys;
     return r.len1 + r.len2;
 }
 // Units of a segment: none for a length outside the cache.
-__device__ __forceinline__ long long dec4_units(int keys, int lead) {
-    return keys > 0 ? static_cast<long long>(keys) + lead : 0;
+__device__ __forceinline__ long long dec4_units(int keys) {
+    return keys > 0 ? static_cast<long long>(keys) + kDec4Lead : 0;
 }
-// Called by a full warp.
+// Units of a block.  Called by a full warp.
 template <bool kMulti>
-__device__ __forceinline__ Dec4Plan dec4_plan(const Decode4Params &p, int lane) {
-    long long keys = 0;
-    int segs = 0;
-    for (int st = lane; st < (kMulti ? p.B * p.n_segs : p.B); st += 32) {
-        const int n = dec4_keys<kMulti>(p, st);
-        keys += n;
-        segs += n > 0;
-    }
+__device__ __forceinline__ long long dec4_share(const Decode4Params &p, int lane) {
+    long long total = 0;
+    for (int st = lane; st < (kMulti ? p.B * p.n_segs : p.B); st += 32) total += dec4_units(dec4_keys<kMulti>(p, st));
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        keys += __shfl_xor_sync(0xffffffffu, keys, off);
-        segs += __shfl_xor_sync(0xffffffffu, segs, off);
-    }
-    keys *= p.Hkv;
-    Dec4Plan plan;
-    plan.lead = keys >= static_cast<long long>(kDec4Chunk) * p.grid_blocks ? kDec4Lead : 0;
-    const long long total = keys + static_cast<long long>(segs) * p.Hkv * plan.lead;
-    const long long even = (total + p.grid_blocks - 1) / p.grid_blocks;
-    plan.U = even > kDec4Chunk ? even : kDec4Chunk;
-    return plan;
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    const long long even = (total * p.Hkv + p.grid_blocks - 1) / p.grid_blocks;
+    return even > kDec4Chunk ? even : kDec4Chunk;
 }
 
 // The new row: rotated, quantised, into slot L of the cache, and its values to k_stored and
@@ -268,8 +252,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     const int val_at0 = dec4_key<HD>(2 * r) * kRow + HD / 2 + (G == 4 ? 8 : 4) * c;
     const int val_at1 = dec4_key<HD>(2 * r + 1) * kRow + HD / 2 + (G == 4 ? 8 : 4) * c;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Dec4Plan plan = dec4_plan<kMulti>(p, lane);
-    const long long u_lo = blockIdx.x * plan.U, u_hi = u_lo + plan.U;
+    const long long U = dec4_share<kMulti>(p, lane);
+    const long long u_lo = blockIdx.x * U, u_hi = u_lo + U;
     if (!kMulti && blockIdx.x == 0)
         for (int b = tid; b < p.B; b += kDec4Threads)
             if (p.cache_len[b] < 0 || p.cache_len[b] > p.T_max - 1) raise_status(kStatusBadCacheLen);
@@ -282,7 +266,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     int st = 0;
     long long seg0 = 0;
     const int n_st = kMulti ? p.B * p.n_segs : p.B;
-    for (long long v; st < n_st && seg0 + (v = p.Hkv * dec4_units(dec4_keys<kMulti>(p, st), plan.lead)) <= u_lo; ++st)
+    for (long long v; st < n_st && seg0 + (v = p.Hkv * dec4_units(dec4_keys<kMulti>(p, st))) <= u_lo; ++st)
         seg0 += v;
     if (st == n_st) return;
     if (tid == 0) {
@@ -298,14 +282,14 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
         const int L = seg.last, b = dec4_sequence<kMulti>(p, st);
         const int t0 = kMulti ? (st - b * p.n_segs) * p.seg_tokens : 0, n_tok = kMulti ? seg.last - seg.first + 1 : 1;
         const int cols = n_tok * g;  // column: token times heads plus head
-        const long long V = dec4_units(rg.len1 + rg.len2, plan.lead);
+        const long long V = dec4_units(rg.len1 + rg.len2);
         if (V == 0) continue;
         int kvh = seg0 < u_lo ? static_cast<int>((u_lo - seg0) / V) : 0;
         seg0 += kvh * V;
         for (; kvh < p.Hkv && seg0 < u_hi; ++kvh, seg0 += V) {
             // Units [u0, u1) of the segment's keys are this block's: keys of the first
             // range, then of the second.
-            const long long k0 = seg0 + plan.lead;
+            const long long k0 = seg0 + kDec4Lead;
             const int u0 = static_cast<int>(max(u_lo, k0) - k0);
             const int u1 = static_cast<int>(min(u_hi, seg0 + V) - k0);
             if (u1 <= 0) continue;
@@ -849,15 +833,15 @@ __global__ void __launch_bounds__(kDec4MergeThreads) decode4_merge_kernel(const 
         if (p.lse != nullptr && tid == 0) p.lse[oi] = __int_as_float(0x7fc00000);
         return;
     }
-    const Dec4Plan plan = dec4_plan<kMulti>(p, lane);
+    const long long U = dec4_share<kMulti>(p, lane);
     long long seg0 = 0;
-    for (int i = lane; i < st; i += 32) seg0 += p.Hkv * dec4_units(dec4_keys<kMulti>(p, i), plan.lead);
+    for (int i = lane; i < st; i += 32) seg0 += p.Hkv * dec4_units(dec4_keys<kMulti>(p, i));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) seg0 += __shfl_xor_sync(0xffffffffu, seg0, off);
-    const long long V = dec4_units(keys, plan.lead);
+    const long long V = dec4_units(keys);
     seg0 += kvh * V;
-    const int first = static_cast<int>((seg0 + plan.lead) / plan.U);
-    const int n = static_cast<int>((seg0 + V - 1) / plan.U) - first + 1;  // pieces, at most one a block
+    const int first = static_cast<int>((seg0 + kDec4Lead) / U);
+    const int n = static_cast<int>((seg0 + V - 1) / U) - first + 1;  // pieces, at most one a block
     const int rows = kMulti ? p.seg_tokens * g : g;
     const long long slot0 = (first + static_cast<long long>(st) * p.Hkv + kvh) * rows + col;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's results
