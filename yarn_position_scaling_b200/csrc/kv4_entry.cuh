@@ -311,13 +311,18 @@ namespace yr_host {
 // prefill kernel, over 16-bit copies of them?  The former reads the rows once for every 16
 // columns (tokens times query heads of a KV head), 60 ps a row (d = 128); the latter makes the
 // copies (110 ps a row) and then holds 256 query rows a tile, with a window 128, however few
-// there are (95 ps a row and query head, with a window half).  Both sides measured after 120K
-// keys of 8 KV heads, 32 query heads: 4 tokens 77 and 464 us, 16 tokens 245 and 465, 32 tokens
-// 469 and 467; with 64 query heads 16 tokens 470 and 809, 32 tokens 922 and 809.
-bool chunk4_by_decode(int g, int Tq, int window) {
+// there are (95 ps a row and query head, with a window half).  At d = 64 the products of the
+// prefill kernel are half as long but its softmax is not.  Both sides measured, decode and
+// prefill kernel: after 120K keys of 8 KV heads with 32 query heads 4 tokens 77 and 464 us, 16
+// tokens 245 and 465, 32 tokens 469 and 467; with 64 query heads 16 tokens 470 and 809, 32
+// tokens 922 and 809; d = 64, 20K keys of 4 KV heads with 16 query heads 40 tokens 46 and 49,
+// 48 tokens 51 and 49; window 4096, d = 128 16 tokens 31 and 34, 24 tokens 36 and 36, d = 64
+// 40 tokens 25 and 28.
+bool chunk4_by_decode(int g, int Tq, int d, int window) {
     if (g > 16) return false;
-    const int passes = decode4_runs(g, Tq).n;
-    return window > 0 ? passes <= 1 + g : 10 * passes <= 17 + 16 * g;
+    const int tenths = 10 * decode4_runs(g, Tq).n;
+    if (d == 64) return tenths <= (window > 0 ? 30 + 15 * g : 20 + 22 * g);
+    return tenths <= (window > 0 ? 10 + 10 * g : 17 + 16 * g);
 }
 
 // Bytes that the decode kernel's partial results take for a chunk.
@@ -371,7 +376,7 @@ extern "C" int yr_attn_prefill_chunk_kv4(const void *q, const void *k_new, const
     rc = launch_kv4_write(k_new, v_new, kv4, B, Hkv, Tq, d, T_max, ks, ks, P0, nullptr, nullptr,
                           tab, sm_count, st);
     if (rc != YR_OK) return rc;
-    if (chunk4_by_decode(Hq / Hkv, Tq, window) &&
+    if (chunk4_by_decode(Hq / Hkv, Tq, d, window) &&
         workspace_bytes >= chunk4_decode_bytes(B, Hq, Hkv, Tq, d)) {
         const Decode4Runs runs = decode4_runs(Hq / Hkv, Tq);
         yr::Decode4Params dp;
