@@ -462,9 +462,10 @@ int yr_attn_decode_noalloc(const void *q_new, const void *k_new, const void *v_n
  *   Codes lie in the order in which the attention reads them, from the low nibble up, with
  *   G = d / 32: 8 key codes at word r G + g (r = 0 .. 3) for elements 32g + 8r .. + 7, and 4
  *   value codes at 16-bit unit c G + g (c = 0 .. 7) for elements 32g + 4c .. + 3.
- * Range: |rotated k| and |v| must stay below 65520.  A value outside (or a NaN) is stored
- *   as the nearest finite fp16 value (a NaN as 65504) and sets a range bit of the device
- *   status word, which yr_device_status() reports as YR_ERANGE.
+ * Range: |rotated k| and |v| must stay below 65520.  A value outside is stored as the
+ *   nearest finite fp16 value, a NaN as some finite value, and a range bit is set in the
+ *   device status word, which yr_device_status() reports as YR_ERANGE; the rest of such a
+ *   32-element group is as coarse as its range asks.
  *
  * kv4_row_bytes -- 5d/4, or 0 if d is not 64 or 128.
  *

@@ -345,6 +345,44 @@ def test_decode_queries_of_any_size(scale):
     assert ((lse[0].double() - rl).abs() <= bl).all()
 
 
+@pytest.mark.parametrize("scale", [0.0, 1e-30, 1e-38])
+def test_decode_alibi_of_queries_that_score_nothing(scale):
+    """ALiBi alone decides: its slope is kept in the units of the scaled query."""
+    gen, d, L = gen_of(16), 64, 700
+    cache = random_rows(gen, 1, 2, L + 1, d)
+    tab = table(d, method="alibi")
+    q = (randn(gen, 1, 8, d) * scale).bfloat16()
+    k, v = (x.squeeze(2) for x in new_kv(gen, 1, 2, 1, d))
+    lse = torch.empty(1, 8, device="cuda")
+    cl = torch.tensor([L], dtype=torch.int32, device="cuda")
+    o = api.attn_decode_kv4(q, k, v, cache, cl, tab, lse=lse)
+    api.device_status()
+    ro, rl, amp, logit = (x.squeeze(1) for x in R.attend(q[0][:, None].double(), cache[0], cl.long(), tab))
+    bo, bl = R.decode_bounds(ro, rl, amp, logit, L + 1, d)
+    # The bias m (L - n) is one more term of the score, rounded with it: up to L at m = 1.
+    slope = 2.0 ** (-torch.arange(1.0, 9.0, device="cuda", dtype=torch.float64))
+    extra = (2.0 ** -22 * slope * L)
+    assert ((o[0].double() - ro).abs() <= bo + (2 * extra)[:, None] * amp).all()
+    assert ((lse[0].double() - rl).abs() <= bl + extra).all()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_decode_keeps_what_is_not_a_number_to_its_head(bad):
+    gen, d, L = gen_of(17), 128, 200
+    tab = table(d)
+    cache = random_rows(gen, 1, 2, L + 1, d)
+    q = randn(gen, 1, 8, d).bfloat16()
+    k, v = (x.squeeze(2) for x in new_kv(gen, 1, 2, 1, d))
+    cl = torch.tensor([L], dtype=torch.int32, device="cuda")
+    want = api.attn_decode_kv4(q, k, v, cache, cl, tab)
+    q[0, 5, 77] = bad
+    got = api.attn_decode_kv4(q, k, v, cache, cl, tab)
+    api.device_status()
+    assert torch.isnan(got[0, 5].float()).all()
+    keep = torch.arange(8, device="cuda") != 5
+    assert torch.equal(got[0, keep], want[0, keep])
+
+
 def test_decode_reports_bad_lengths():
     gen, d = gen_of(14), 64
     cache = random_rows(gen, 4, 2, 50, d)

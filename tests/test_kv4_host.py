@@ -123,6 +123,14 @@ def test_sizes(lib):
     split = api.attn_prefill_chunk_split_bytes(1, 32, 256, 128)
     assert api.attn_prefill_chunk_kv4_workspace_bytes(1, 32, 8, 256, 128, 1000) == planes + split
     assert api.attn_prefill_chunk_kv4_workspace_bytes(1, 32, 8, 256, 128, -1) == 0
+    # a few tokens: room for a partial result of each block and segment, 16 rows of d + 2 each
+    few = api.attn_prefill_chunk_kv4_workspace_bytes(1, 32, 8, 4, 128, 0)
+    assert few >= (592 + 8) * 16 * 130 * 4
+    huge = (1 << 29) + 5  # sizes whose products pass 32 bits
+    planes = api.attn_prefill_workspace_bytes(1, 1, huge, 64)
+    split = api.attn_prefill_chunk_split_bytes(1, 16, huge, 64)
+    assert api.attn_prefill_chunk_kv4_workspace_bytes(1, 16, 1, huge, 64, 0) == \
+        (planes + 255) // 256 * 256 + split
     assert api.attn_prefill_chunk_kv4_workspace_bytes(1, 32, 8, 256, 128, 1 << 30) == 0
 
 

@@ -1,11 +1,11 @@
-// decode4_sm100.cuh -- single-token decode over the 4-bit KV cache (row format in
-// kv4_sm100.cuh), split-KV with a log-sum-exp merge.
+// decode4_sm100.cuh -- decode over the 4-bit KV cache (row format in kv4_sm100.cuh), one token
+// or a few, split-KV with a log-sum-exp merge.
 //
 //   logit(t) = scale q~ . k_t,  k_t = s n + z by group;  o = sum_t p_t v_t / sum_t p_t
 //
-// The visible keys of all (sequence, KV head) segments, laid end to end, are cut into one
-// equal share per block; a block leaves one partial (max, sum, unnormalised output) per
-// query head and segment piece.  Pieces are numbered block + segment: along the blocks
+// The keys that the tokens of a (sequence, KV head) segment see, of all segments laid end to
+// end, are cut into one equal share per block; a block leaves one partial (reference, sum,
+// unnormalised output) per query head and token of each segment piece.  Pieces are numbered block + segment: along the blocks
 // each next piece raises the one, the other or both, so no two share a number, and
 // blocks + segments slots hold them all whatever the lengths.
 #pragma once
@@ -393,8 +393,9 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
 #pragma unroll
                 for (int off = 1; off < HD / 8; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                 // Largest element to [2^7, 2^8): both parts and their group sums fit fp16,
-                // and the second part keeps its bits.
-                const int e2 = mx > 0.f ? max(-100, min(127, exponent_of(mx))) : 0;
+                // and the second part keeps its bits.  (Below 2^-60 a query scores 0 anyway, and
+                // ALiBi's slope in these units has to stay within fp32.)
+                const int e2 = mx > 0.f ? max(-60, min(127, exponent_of(mx))) : 0;
                 const float f = pow2i(7 - e2);
                 // The fragment words of lane r = ch % 4 for group ch / 4: word 2 part + k
                 // holds elements 2 part + k and, above it, 4 further on; those of k = 1 meet

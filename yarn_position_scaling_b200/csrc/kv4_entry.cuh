@@ -103,7 +103,7 @@ struct Decode4Runs {
     int tokens, n;
 };
 Decode4Runs decode4_runs(int g, int Tq) {
-    const int cols = Tq * g <= 8 ? 8 : 16;
+    const int cols = static_cast<long long>(Tq) * g <= 8 ? 8 : 16;
     int tokens = cols / g < Tq ? cols / g : Tq;
     if (tokens < 1) tokens = 1;
     tokens = (Tq + (Tq + tokens - 1) / tokens - 1) / ((Tq + tokens - 1) / tokens);  // evenly
@@ -320,7 +320,7 @@ namespace yr_host {
 // 40 tokens 25 and 28.
 bool chunk4_by_decode(int g, int Tq, int d, int window) {
     if (g > 16) return false;
-    const int tenths = 10 * decode4_runs(g, Tq).n;
+    const long long tenths = 10ll * decode4_runs(g, Tq).n;
     if (d == 64) return tenths <= (window > 0 ? 30 + 15 * g : 20 + 22 * g);
     return tenths <= (window > 0 ? 10 + 10 * g : 17 + 16 * g);
 }
@@ -341,7 +341,9 @@ extern "C" size_t yr_attn_prefill_chunk_kv4_workspace_bytes(int B, int Hq, int H
         return 0;
     const size_t prefill = round256(prefill_ws_bytes(B, Hkv, static_cast<long long>(P0) + Tq, d)) +
                            kMaxSplit * split_share_bytes(B, Hq, Tq, d);
-    const size_t decode = Hq / Hkv <= 16 ? chunk4_decode_bytes(B, Hq, Hkv, Tq, d) : 0;
+    const int g = Hq / Hkv;
+    const bool by_decode = chunk4_by_decode(g, Tq, d, 0) || chunk4_by_decode(g, Tq, d, 1);
+    const size_t decode = by_decode ? chunk4_decode_bytes(B, Hq, Hkv, Tq, d) : 0;
     return prefill > decode ? prefill : decode;
 }
 
@@ -377,6 +379,7 @@ extern "C" int yr_attn_prefill_chunk_kv4(const void *q, const void *k_new, const
                           tab, sm_count, st);
     if (rc != YR_OK) return rc;
     if (chunk4_by_decode(Hq / Hkv, Tq, d, window) &&
+        static_cast<long long>(B) * Hq * Tq < (1ll << 31) &&
         workspace_bytes >= chunk4_decode_bytes(B, Hq, Hkv, Tq, d)) {
         const Decode4Runs runs = decode4_runs(Hq / Hkv, Tq);
         yr::Decode4Params dp;
