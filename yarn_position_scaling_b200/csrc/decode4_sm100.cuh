@@ -263,12 +263,28 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     const uint64_t policy = l2_policy_evict_first();
 
     // Segments before the first one of this block.
+    // 32 at a time, by a sum over the lanes.
     int st = 0;
     long long seg0 = 0;
     const int n_st = kMulti ? p.B * p.n_segs : p.B;
-    for (long long v; st < n_st && seg0 + (v = p.Hkv * dec4_units(dec4_keys<kMulti>(p, st))) <= u_lo; ++st)
-        seg0 += v;
-    if (st == n_st) return;
+    for (; st < n_st; st += 32) {
+        const long long v = st + lane < n_st ? p.Hkv * dec4_units(dec4_keys<kMulti>(p, st + lane)) : 0;
+        long long upto = v;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += t;
+        }
+        const uint32_t beyond = __ballot_sync(0xffffffffu, seg0 + upto > u_lo);
+        if (beyond != 0) {
+            const int at = __ffs(beyond) - 1;
+            seg0 += __shfl_sync(0xffffffffu, upto - v, at);
+            st += at;
+            break;
+        }
+        seg0 += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (st >= n_st) return;
     if (tid == 0) {
         for (int w = 0; w < kDec4Warps; ++w)
             for (int s = 0; s < kDec4Stages; ++s) mbar_init(&sm->full[w][s], 1);
