@@ -471,31 +471,32 @@ def kv4_cache(B: int, Hkv: int, T_max: int, d: int, device="cuda") -> torch.Tens
 # The calls below are made once per layer and token, so what they do in Python is kept short:
 # pointers go over as plain integers and the current stream's handle is asked for directly.
 def _kv4_cache_of(fn, kv4, B, Hkv, d):
-    """Checks the cache and returns its device."""
-    if not kv4.is_cuda or kv4.dtype != torch.uint8 or kv4.dim() != 4 or not kv4.is_contiguous():
+    """Checks the cache and returns its device's index."""
+    if not kv4.is_cuda or kv4.dtype is not torch.uint8 or kv4.dim() != 4 or not kv4.is_contiguous():
         raise ValueError(f"{fn}: kv4 must be a contiguous uint8 CUDA tensor [B, Hkv, T_max, 5d/4]")
-    if kv4.shape[0] != B or kv4.shape[1] != Hkv or kv4.shape[3] * 4 != 5 * d:
+    b, h, _, n = kv4.shape
+    if b != B or h != Hkv or n * 4 != 5 * d:
         raise ValueError(f"{fn}: kv4 must have the shape {(B, Hkv, 'T_max', 5 * d / 4)}, "
                          f"not {tuple(kv4.shape)}")
-    return kv4.device
+    return kv4.get_device()
 
 
 def _kv4_arg(fn, name, t, dev, dtype, shape, strided=False):
     """The address of tensor t after checking it (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{fn}: {name} must be a {dtype} tensor on {dev}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} must be a {dtype} tensor on cuda:{dev}")
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} must have the shape {shape}, not {tuple(t.shape)}")
-    if not strided and not t.is_contiguous():
+    if not (strided or t.is_contiguous()):
         raise ValueError(f"{fn}: {name} must be contiguous")
     return t.data_ptr()
 
 
 def _kv4_workspace(fn, ws, dev):
-    if ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be a contiguous tensor on {dev}")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous tensor on cuda:{dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -518,8 +519,8 @@ def _kv4_call(dev, fn, args, stream):
     if stream is not None:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     else:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    if dev.index == torch._C._cuda_getDevice():
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
         _check(fn(*args, handle))
     else:
         with torch.cuda.device(dev):

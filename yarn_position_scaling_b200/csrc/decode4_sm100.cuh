@@ -22,7 +22,6 @@ constexpr int kDec4Threads = kDec4Warps * 32;
 constexpr int kDec4Tile = 32;  // keys of one bulk copy
 constexpr int kDec4Stages = 2;
 constexpr float kNoScore = -1e30f;  // the reference of a column that has seen no key yet
-constexpr int kDec4Step = 32;  // keys that a warp takes through scores and outputs at a time
 
 struct Decode4Params {
     const __nv_bfloat16 *q_new;          // [B][Hq][Tq][d]
@@ -195,13 +194,14 @@ __device__ __forceinline__ int dec4_key(int i) {
         return (i & 8) + 2 * (i & 3) + h;
 }
 
-template <int HD, int NT>
+// (Kept small: what shared memory leaves of an SM's 256 KB is the L1 that spills live in.)
+template <int HD, int NT, bool kMulti>
 struct Decode4Smem {
     static constexpr int kStageBytes = kDec4Tile * kv4_row_bytes(HD);
     alignas(128) uint8_t ring[kDec4Warps][kDec4Stages][kStageBytes];  // also the warps' outputs
     alignas(16) uint8_t new_row[kv4_row_bytes(HD)];
     double2 cs[HD / 2];
-    float2 q_cs[8 * NT][HD / 2];  // by token
+    float2 q_cs[kMulti ? 8 * NT : 1][HD / 2];  // by token
     uint4 q_hi[8 * NT][HD / 8], q_lo[8 * NT][HD / 8];  // fragments, see the rotation below
     float q_sum[8 * NT][HD / kKv4Group];  // sums of the scaled query over the groups
     float q_scale[8 * NT];  // what takes the scaled query back
@@ -210,9 +210,9 @@ struct Decode4Smem {
     uint64_t full[kDec4Warps][kDec4Stages];
     int abort;
 };
-template <int HD, int NT>
+template <int HD, int NT, bool kMulti>
 constexpr size_t decode4_smem_bytes() {
-    return sizeof(Decode4Smem<HD, NT>) + 128;
+    return sizeof(Decode4Smem<HD, NT, kMulti>) + 128;
 }
 
 // Each warp takes every fourth 32-key tile of the block's share by itself: a ring of bulk
@@ -235,10 +235,13 @@ constexpr size_t decode4_smem_bytes() {
 template <int HD, int NT, int REP, bool kHalf, bool kMulti>
 __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     decode4_split_kernel(const __grid_constant__ Decode4Params p) {
-    using Smem = Decode4Smem<HD, NT>;
+    using Smem = Decode4Smem<HD, NT, kMulti>;
     constexpr int kRow = kv4_row_bytes(HD), G = HD / kKv4Group;
     static_assert(REP == 1 || (NT == 1 && REP <= G), "columns to spare");
-    constexpr int H = kDec4Step / 16;
+    // A step takes 16 H keys through scores and outputs.  Two halves overlap; with one query head
+    // a KV head, where the work on p s is least, one at a time spills less (77 against 81 us on
+    // 16 windowed sequences of 32 KV heads, but 175 against 167 on 8 long ones with REP = 2).
+    constexpr int H = REP == 4 ? 1 : 2;
     constexpr int GL = G / REP;       // groups of a lane in the value product: k REP + copy
     constexpr int kCopy = 4 / REP;    // lanes r of a copy; the next copy is as far away
     extern __shared__ uint8_t smem_raw[];
@@ -478,7 +481,12 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 for (int j = 0; j < 2; ++j) x_scale[nt][j] = p.sl2 * sm->q_scale[nt * 8 + 2 * (r % kCopy) + j];
             }
 
-            float o[G][2][NT][4], w[NT][2][GL], l[NT][2], R[NT][2];
+            // With kShare the outputs of group k REP + copy are in o[k]: the copies' columns take
+            // turns, each group's B operand being zero in the others'.  It saves registers (d =
+            // 128: 175 -> 167 us); where there are enough, the zeroing costs more (d = 64: 78 -> 81).
+            constexpr bool kShare = REP > 1 && HD == 128;
+            constexpr int GO = kShare ? GL : G;
+            float o[GO][2][NT][4], w[NT][2][GL], l[NT][2], R[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -488,9 +496,9 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
 #pragma unroll
                     for (int k = 0; k < GL; ++k) w[nt][j][k] = 0.f;
 #pragma unroll
-                    for (int gr = 0; gr < G; ++gr) {
-                        o[gr][0][nt][j] = o[gr][0][nt][j + 2] = 0.f;
-                        o[gr][1][nt][j] = o[gr][1][nt][j + 2] = 0.f;
+                    for (int k = 0; k < GO; ++k) {
+                        o[k][0][nt][j] = o[k][0][nt][j + 2] = 0.f;
+                        o[k][1][nt][j] = o[k][1][nt][j + 2] = 0.f;
                     }
                 }
 
@@ -712,11 +720,11 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
 #pragma unroll
                             for (int i = 0; i < GL; ++i) w[nt][j][i] *= f;
 #pragma unroll
-                            for (int gr = 0; gr < G; ++gr) {
-                                o[gr][0][nt][j] *= f;
-                                o[gr][0][nt][j + 2] *= f;
-                                o[gr][1][nt][j] *= f;
-                                o[gr][1][nt][j + 2] *= f;
+                            for (int i = 0; i < GO; ++i) {
+                                o[i][0][nt][j] *= f;
+                                o[i][0][nt][j + 2] *= f;
+                                o[i][1][nt][j] *= f;
+                                o[i][1][nt][j + 2] *= f;
                             }
                         }
                     products();
@@ -758,8 +766,10 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                         const uint32_t us = u >> 8, vs = v >> 8;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16_16816(o[gr][0][nt], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0[gr / REP][nt], b1[gr / REP][nt]);
-                            mma_f16_16816(o[gr][1][nt], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, b0[gr / REP][nt], b1[gr / REP][nt]);
+                            const bool mine = !kShare || c / (8 / REP) == gr % REP;
+                            const uint32_t b0g = mine ? b0[gr / REP][nt] : 0u, b1g = mine ? b1[gr / REP][nt] : 0u;
+                            mma_f16_16816(o[kShare ? gr / REP : gr][0][nt], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0g, b1g);
+                            mma_f16_16816(o[kShare ? gr / REP : gr][1][nt], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, b0g, b1g);
                         }
                     }
                 }
@@ -790,17 +800,18 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
             if (sm->abort) return;  // a copy did not land: no partial result to trust
             float *red = reinterpret_cast<float *>(&sm->ring[0][0][0]);  // [warps][8 NT][HD]
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                if (gr % REP != copy) continue;  // another copy's group
+            for (int i = 0; i < GO; ++i) {
+                if (!kShare && i % REP != copy) continue;  // another copy's group
+                const int gr = kShare ? i * REP + copy : i;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float add = w[nt][j][gr / REP];
-                        const float4 out = make_float4(fmaf(o[gr][0][nt][j], 16777216.f, add),
-                                                       fmaf(o[gr][0][nt][j + 2], 1048576.f, add),
-                                                       fmaf(o[gr][1][nt][j], 16777216.f, add),
-                                                       fmaf(o[gr][1][nt][j + 2], 1048576.f, add));
+                        const float add = w[nt][j][kShare ? i : i / REP];
+                        const float4 out = make_float4(fmaf(o[i][0][nt][j], 16777216.f, add),
+                                                       fmaf(o[i][0][nt][j + 2], 1048576.f, add),
+                                                       fmaf(o[i][1][nt][j], 16777216.f, add),
+                                                       fmaf(o[i][1][nt][j + 2], 1048576.f, add));
                         *reinterpret_cast<float4 *>(red + (warp * 8 * NT + nt * 8 + 2 * (r % kCopy) + j) * HD + 32 * gr + 4 * c) = out;
                     }
             }

@@ -118,7 +118,7 @@ int launch_decode4_form(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
         int n = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
                 &n, yr::decode4_split_kernel<HD, NT, REP, kHalf, kMulti>, yr::kDec4Threads,
-                yr::decode4_smem_bytes<HD, NT>()) != cudaSuccess ||
+                yr::decode4_smem_bytes<HD, NT, kMulti>()) != cudaSuccess ||
             n < 1)
             n = 1;
         per_sm = n;
@@ -128,7 +128,7 @@ int launch_decode4_form(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
     const long long slots = dp.grid_blocks + static_cast<long long>(dp.B) * dp.n_segs * dp.Hkv;
     dp.ws_ml = dp.ws_o + slots * dp.seg_tokens * dp.group * HD;
     yr::decode4_split_kernel<HD, NT, REP, kHalf, kMulti>
-        <<<dp.grid_blocks, yr::kDec4Threads, yr::decode4_smem_bytes<HD, NT>(), st>>>(dp);
+        <<<dp.grid_blocks, yr::kDec4Threads, yr::decode4_smem_bytes<HD, NT, kMulti>(), st>>>(dp);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("decode4_split_kernel launch", e);
     return YR_OK;

@@ -152,11 +152,11 @@ int prepare_device(int *sm_count, DeviceState *out = nullptr) {
                  yr::decode_smem_bytes<64>()},
                 {reinterpret_cast<const void *>(&yr::decode_split_kernel<64, 2>),
                  yr::decode_smem_bytes<64>()},
-#define YR_DECODE4(HD, NT, REP, kHalf)                                                     \
-    {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, kHalf, false>), \
-     yr::decode4_smem_bytes<HD, NT>()},                                                    \
+#define YR_DECODE4(HD, NT, REP, kHalf)                                                        \
+    {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, kHalf, false>),    \
+     yr::decode4_smem_bytes<HD, NT, false>()},                                                \
         {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, kHalf, true>), \
-         yr::decode4_smem_bytes<HD, NT>()}
+         yr::decode4_smem_bytes<HD, NT, true>()}
                 YR_DECODE4(128, 1, 4, false), YR_DECODE4(128, 1, 4, true),
                 YR_DECODE4(128, 1, 2, false), YR_DECODE4(128, 1, 2, true),
                 YR_DECODE4(128, 1, 1, false), YR_DECODE4(128, 1, 1, true),
