@@ -199,9 +199,9 @@ template <int HD, int NT, bool kMulti>
 struct Decode4Smem {
     static constexpr int kStageBytes = kDec4Tile * kv4_row_bytes(HD);
     alignas(128) uint8_t ring[kDec4Warps][kDec4Stages][kStageBytes];  // also the warps' outputs
-    alignas(16) uint8_t new_row[kv4_row_bytes(HD)];
-    double2 cs[HD / 2];
-    float2 q_cs[kMulti ? 8 * NT : 1][HD / 2];  // by token
+    alignas(16) uint8_t new_row[kMulti ? 16 : kv4_row_bytes(HD)];
+    double2 cs[kMulti ? 1 : HD / 2];   // of the one token, for the new row
+    float2 q_cs[kMulti ? 1 : HD / 2];  // and for the queries
     uint4 q_hi[8 * NT][HD / 8], q_lo[8 * NT][HD / 8];  // fragments, see the rotation below
     float q_sum[8 * NT][HD / kKv4Group];  // sums of the scaled query over the groups
     float q_scale[8 * NT];  // what takes the scaled query back
@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
         const Dec4Seg seg = dec4_seg<kMulti>(p, st);
         const DecRanges rg = seg.keys;
         const int L = seg.last, b = dec4_sequence<kMulti>(p, st);
-        const int t0 = kMulti ? (st - b * p.n_segs) * p.seg_tokens : 0, n_tok = kMulti ? seg.last - seg.first + 1 : 1;
-        const int cols = n_tok * g;  // column: token times heads plus head
+        const int t0 = kMulti ? (st - b * p.n_segs) * p.seg_tokens : 0;
+        const int cols = (kMulti ? seg.last - seg.first + 1 : 1) * g;  // column: token times heads plus head
         const long long V = dec4_units(rg.len1 + rg.len2);
         if (V == 0) continue;
         int kvh = seg0 < u_lo ? static_cast<int>((u_lo - seg0) / V) : 0;
@@ -368,41 +368,46 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                     if (kHalf) other[n] = __ldg(row + (ch ^ (HD / 16)));
                 }
             }
-            // The new row wants its sines in 64 bits; the queries' 22 bits do with fp32 ones.
-            for (int n = tid; n < n_tok * (HD / 2); n += kDec4Threads) {
-                const int i = n % (HD / 2), tok = n / (HD / 2);
-                if (has_L) {
-                    const double2 t = kv4_cos_sin(L, p.turns[i]);
-                    sm->cs[i] = t;
-                    sm->q_cs[0][i] = make_float2(static_cast<float>(t.x), static_cast<float>(t.y));
-                } else {
-                    const double tr = static_cast<double>(seg.first + tok) * p.turns[i];
-                    float sn, co;
-                    sincospif(2.f * static_cast<float>(tr - rint(tr)), &sn, &co);
-                    sm->q_cs[tok][i] = make_float2(co, sn);
+            // The new row wants its sines in 64 bits; the queries' 22 bits do with fp32 ones.  Of
+            // one token they are shared by its heads, of several each thread computes its own.
+            auto cos_sin = [&](int pos, int i) {
+                const double tr = static_cast<double>(pos) * p.turns[i];
+                float sn, co;
+                sincospif(2.f * static_cast<float>(tr - rint(tr)), &sn, &co);
+                return make_float2(co, sn);
+            };
+            if constexpr (!kMulti) {
+                for (int i = tid; i < HD / 2; i += kDec4Threads) {
+                    if (has_L) {
+                        const double2 t = kv4_cos_sin(L, p.turns[i]);
+                        sm->cs[i] = t;
+                        sm->q_cs[i] = make_float2(static_cast<float>(t.x), static_cast<float>(t.y));
+                    } else {
+                        sm->q_cs[i] = cos_sin(L, i);
+                    }
                 }
+                __syncthreads();
             }
-            __syncthreads();
 #pragma unroll
             for (int n = 0; n < kPer; ++n) {
                 const int i = tid + n * kDec4Threads, h = i / (HD / 8), ch = i % (HD / 8);
                 if (i >= kItems) break;
                 float x[8], y[8], mx = 0.f;
                 unpack_bf16x8(raw[n], x);
-                const float2 *cs = sm->q_cs[h < cols ? dec4_token<kMulti>(p, h) : 0];
+                const int pos = seg.first + dec4_token<kMulti>(p, h);
                 if constexpr (kHalf) {
                     float z[8];
                     unpack_bf16x8(other[n], z);
                     const int c0 = 8 * (ch % (HD / 16));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float2 t = cs[c0 + e];
+                        const float2 t = kMulti ? cos_sin(pos, c0 + e) : sm->q_cs[c0 + e];
                         y[e] = ch < HD / 16 ? x[e] * t.x - z[e] * t.y : z[e] * t.y + x[e] * t.x;
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 t = cs[4 * ch + e];
+                        const float2 t = kMulti ? cos_sin(pos, 4 * ch + e) : sm->q_cs[4 * ch + e];
                         y[2 * e] = x[2 * e] * t.x - x[2 * e + 1] * t.y;
                         y[2 * e + 1] = x[2 * e] * t.y + x[2 * e + 1] * t.x;
                     }
