@@ -671,6 +671,37 @@ def test_results_repeat_bit_for_bit_and_on_another_stream():
     assert torch.equal(a, kr) and torch.equal(b, vr)
 
 
+def test_stream_argument_with_outputs_allocated_by_the_call():
+    """The call's own outputs and workspaces belong to the stream it runs on, whatever the
+    current stream frees and takes meanwhile."""
+    tab = table(128)
+    q, k, v, cache, cl = _decode_case(43)
+    want = api.attn_decode_kv4(q, k, v, cache, cl, tab)
+    kw, vw = api.kv4_read(cache, 500)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        for _ in range(20):
+            got = api.attn_decode_kv4(q, k, v, cache, cl, tab, stream=stream)
+            kr, vr = api.kv4_read(cache, 500, stream=stream)
+            churn = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+            del churn
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(kr, kw) and torch.equal(vr, vw)
+
+
+def test_read_of_keys_or_values_alone():
+    gen, d = gen_of(44), 64
+    cache = random_rows(gen, 1, 2, 40, d)
+    kw, vw = api.kv4_read(cache, 30, pos0=3)
+    one = torch.zeros_like(kw)
+    k, v = api.kv4_read(cache, 30, pos0=3, k=one)
+    assert k is one and v is None and torch.equal(one, kw)
+    k, v = api.kv4_read(cache, 30, pos0=3, v=one)
+    assert k is None and v is one and torch.equal(one, vw)
+    api.device_status()
+
+
 def test_two_calls_at_once_with_a_workspace_each():
     tab = table(128)
     cases = [_decode_case(51), _decode_case(52, 5000)]

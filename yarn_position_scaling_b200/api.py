@@ -500,10 +500,22 @@ def _kv4_workspace(fn, ws, dev):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _kv4_empty(shape, dtype, dev, stream):
+    """An output or workspace allocated here, on the stream that the call runs on: freed, it goes
+    to that stream's later work only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _kv4_strides(fn, name, t):
-    """Strides over b, h and t, or None if contiguous.  Those of axes of one element are never
-    used and may be anything in torch; they are passed on as those of a contiguous tensor."""
-    if t.is_contiguous():
+    """Strides over b, h and t, or None if contiguous (or left out).  Those of axes of one element
+    are never used and may be anything in torch; they are passed on as those of a contiguous
+    tensor."""
+    if t is None or t.is_contiguous():
         return None
     if t.stride(3) != 1:
         raise ValueError(f"{fn}: {name} must have unit stride over d")
@@ -548,9 +560,9 @@ def kv4_read(kv4, T: int, pos0: int = 0, starts=None, counts=None, dtype=torch.b
              k=None, v=None, stream=None):
     """Rows of the 4-bit cache as values: row t of sequence b from slot pos0 + starts[b] + t,
     t < counts[b] (starts, counts as in kv4_write).  Returns (k, v) [B,Hkv,T,d] in `dtype`
-    (bf16 or fp16); outputs given as k and v are written in place (any strides with unit
-    stride over d) and keep the rows that are not read, others are allocated, with zeros
-    there."""
+    (bf16 or fp16), zero in the rows that are not read.  Outputs given as k and v are written
+    in place (any strides with unit stride over d) and keep those rows; if one is given, the
+    other is not read and comes back as None."""
     fn = "kv4_read"
     if dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("kv4_read: dtype must be torch.bfloat16 or torch.float16")
@@ -559,17 +571,16 @@ def kv4_read(kv4, T: int, pos0: int = 0, starts=None, counts=None, dtype=torch.b
     dev = _kv4_cache_of(fn, kv4, B, Hkv, d)
     shape, zero_rest = (B, Hkv, T, d), k is None and v is None
     if zero_rest:
-        k = torch.empty(shape, dtype=dtype, device=dev)
-        v = torch.empty(shape, dtype=dtype, device=dev)
-    elif k is None:
-        k = torch.zeros(shape, dtype=dtype, device=dev)
-    elif v is None:
-        v = torch.zeros(shape, dtype=dtype, device=dev)
+        k = _kv4_empty(shape, dtype, dev, stream)
+        v = _kv4_empty(shape, dtype, dev, stream)
+        outs, strides = (k.data_ptr(), v.data_ptr()), (None, None)
+    else:
+        outs = (_kv4_arg(fn, "k", k, dev, dtype, shape, True),
+                _kv4_arg(fn, "v", v, dev, dtype, shape, True))
+        strides = (_kv4_strides(fn, "k", k), _kv4_strides(fn, "v", v))
     _kv4_call(dev, load().yr_kv4_read,
-              (kv4.data_ptr(), _kv4_arg(fn, "k", k, dev, dtype, shape, True),
-               _kv4_arg(fn, "v", v, dev, dtype, shape, True),
-               KV4_BF16 if dtype == torch.bfloat16 else KV4_FP16, B, Hkv, T, d, T_max,
-               _kv4_strides(fn, "k", k), _kv4_strides(fn, "v", v), int(pos0),
+              (kv4.data_ptr(), *outs, KV4_BF16 if dtype is torch.bfloat16 else KV4_FP16, B, Hkv,
+               T, d, T_max, *strides, int(pos0),
                _kv4_arg(fn, "starts", starts, dev, torch.int32, (B,)),
                _kv4_arg(fn, "counts", counts, dev, torch.int32, (B,)), int(zero_rest)), stream)
     return k, v
@@ -591,10 +602,10 @@ def attn_decode_kv4(q_new, k_new, v_new, kv4, cache_len, table: RopeTable, windo
     Hkv, T_max = kv4.shape[1], kv4.shape[2]
     dev = _kv4_cache_of(fn, kv4, B, Hkv, d)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=bf, device=dev)
+        out = _kv4_empty((B, Hq, d), bf, dev, stream)
     if workspace is None:
-        workspace = torch.empty(attn_decode_kv4_workspace_bytes(B, Hq, Hkv, d),
-                                dtype=torch.uint8, device=dev)
+        workspace = _kv4_empty(attn_decode_kv4_workspace_bytes(B, Hq, Hkv, d), torch.uint8, dev,
+                               stream)
     sq, sk = (B, Hq, d), (B, Hkv, d)
     _kv4_call(dev, load().yr_attn_decode_kv4,
               (_kv4_arg(fn, "q_new", q_new, dev, bf, sq), _kv4_arg(fn, "k_new", k_new, dev, bf, sk),
@@ -624,11 +635,11 @@ def attn_prefill_chunk_kv4(q, k_new, v_new, kv4, P0: int, table: RopeTable, wind
     Hkv, T_max = kv4.shape[1], kv4.shape[2]
     dev = _kv4_cache_of(fn, kv4, B, Hkv, d)
     if out is None:
-        out = torch.empty((B, Hq, Tq, d), dtype=bf, device=dev)
+        out = _kv4_empty((B, Hq, Tq, d), bf, dev, stream)
     if workspace is None:
-        workspace = torch.empty(
-            attn_prefill_chunk_kv4_workspace_bytes(B, Hq, Hkv, Tq, d, int(P0)),
-            dtype=torch.uint8, device=dev)
+        workspace = _kv4_empty(
+            attn_prefill_chunk_kv4_workspace_bytes(B, Hq, Hkv, Tq, d, int(P0)), torch.uint8, dev,
+            stream)
     sq, sk = (B, Hq, Tq, d), (B, Hkv, Tq, d)
     _kv4_call(dev, load().yr_attn_prefill_chunk_kv4,
               (_kv4_arg(fn, "q", q, dev, bf, sq), _kv4_arg(fn, "k_new", k_new, dev, bf, sk),
