@@ -228,8 +228,8 @@ constexpr size_t decode4_smem_bytes() {
 //   REP of the eight.  Every second of them takes the query's second part, whose scores are
 //   then added across lanes, and each stands for its own groups in the value product, which
 //   divides the work on p s among the lanes that would else idle.
-//   Outputs: O^T[16 dims x 8 heads], value codes as A in the same way (a byte's two codes as a
-//   whole, and the upper one), B = p s in fp16; sum p z in fp32.  p = 2^(score - R) for a reference R per head that puts the largest p s of
+//   Outputs: O^T[16 dims x 8 heads], value codes as A in the same way, B = p s in fp16; sum
+//   p z in fp32.  p = 2^(score - R) for a reference R per head that puts the largest p s of
 //   a tile at 2^8 and is raised only once one passes 2^15: small scales keep their bits
 //   (fp16 holds 2^-14 at full precision), and the common tile costs one vote.
 template <int HD, int NT, int REP, bool kHalf, bool kMulti>
@@ -768,15 +768,13 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                         const uint32_t sel = gr & 1 ? 0x7632u : 0x5410u;
                         const uint32_t u = __byte_perm(vw[0][gr / 2], vw[1][gr / 2], sel);
                         const uint32_t v = __byte_perm(vw[2][gr / 2], vw[3][gr / 2], sel);
-                        // A byte's two codes a, b as the rows a + 16 b and 16 b, whose outputs are
-                        // taken apart at the end: the upper bytes' shift is their mask.
-                        const uint32_t us = __byte_perm(u, 0, 0x4341), vs = __byte_perm(v, 0, 0x4341);
+                        const uint32_t us = u >> 8, vs = v >> 8;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const bool mine = !kShare || c / (8 / REP) == gr % REP;
                             const uint32_t b0g = mine ? b0[gr / REP][nt] : 0u, b1g = mine ? b1[gr / REP][nt] : 0u;
-                            mma_f16_16816(o[kShare ? gr / REP : gr][0][nt], u & 0x00ff00ffu, u & 0x00f000f0u, v & 0x00ff00ffu, v & 0x00f000f0u, b0g, b1g);
-                            mma_f16_16816(o[kShare ? gr / REP : gr][1][nt], us, us & 0x00f000f0u, vs, vs & 0x00f000f0u, b0g, b1g);
+                            mma_f16_16816(o[kShare ? gr / REP : gr][0][nt], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0g, b1g);
+                            mma_f16_16816(o[kShare ? gr / REP : gr][1][nt], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, b0g, b1g);
                         }
                     }
                 }
@@ -815,9 +813,9 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float add = w[nt][j][kShare ? i : i / REP];
-                        const float4 out = make_float4(fmaf(o[i][0][nt][j] - o[i][0][nt][j + 2], 16777216.f, add),
+                        const float4 out = make_float4(fmaf(o[i][0][nt][j], 16777216.f, add),
                                                        fmaf(o[i][0][nt][j + 2], 1048576.f, add),
-                                                       fmaf(o[i][1][nt][j] - o[i][1][nt][j + 2], 16777216.f, add),
+                                                       fmaf(o[i][1][nt][j], 16777216.f, add),
                                                        fmaf(o[i][1][nt][j + 2], 1048576.f, add));
                         *reinterpret_cast<float4 *>(red + (warp * 8 * NT + nt * 8 + 2 * (r % kCopy) + j) * HD + 32 * gr + 4 * c) = out;
                     }
