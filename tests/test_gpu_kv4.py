@@ -296,6 +296,38 @@ def test_decode_many_and_single_sequences():
     run_decode(gen_of(8), 4, 1, 128, [30000], 30001)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_sums_over_many_keys_do_not_drift(d):
+    """Values of both signs cancel over 128K keys of like weight, while the codes' own sums only
+    grow, and the tensor cores cut their sums off: each 16 keys take up to two units in the last
+    place, 2^-22, off a sum that grows evenly over the 512 keys between two folds, 32 / 2 times
+    2^-22 of it in all.  That part has one sign: seen in the mean over heads and dimensions, where
+    the roundings to nearest (p s to 2^-11 of terms that add up like the root of their number, o
+    to 2^-8) are left as their six standard deviations."""
+    B, H, L = 24, 8, 131071
+    gen, tab = gen_of(30 + d), table(d)
+    rows = torch.empty(H, L + 1, 5 * d // 4, dtype=torch.uint8, device="cuda")
+    rows[..., :d] = torch.randint(0, 256, (H, L + 1, d), generator=gen, dtype=torch.uint8, device="cuda")
+    s = (0.5 + 0.5 * torch.rand(H, L + 1, d // 16, generator=gen, device="cuda")).half()
+    par = torch.stack([s, -7.5 * s], -1).flatten(-2)
+    par[..., : d // 16] *= 0.25  # keys
+    rows[..., d:] = par.view(torch.uint8)
+    cache = rows.expand(B, -1, -1, -1).contiguous()
+    q, k = randn(gen, H, d).bfloat16(), randn(gen, H, d).bfloat16()
+    o = api.attn_decode_kv4(*(x.expand(B, -1, -1).contiguous() for x in (q, k, k)), cache,
+                            torch.full((B,), L, dtype=torch.int32, device="cuda"), tab)
+    api.device_status()
+    pos = torch.tensor([L], device="cuda")
+    ro, _, amp, _ = (x.squeeze(1) for x in R.attend(R.rotate(q[:, None], pos, tab), cache[0], pos, tab))
+    n_out = ro.numel()
+    # Codes up to 15; sum p^2 taken as 4 / keys (scores of deviation 1 give e / keys).
+    terms = 2.0 ** -11 / 3 ** 0.5 * 15 * (4 / L) ** 0.5 / n_out ** 0.5
+    rounding = 2.0 ** -8 / 3 ** 0.5 * float(ro.pow(2).mean().sqrt()) / n_out ** 0.5
+    bound = 16 * 2.0 ** -22 * float(amp.mean()) + 6 * (terms + rounding)
+    for b in (0, B // 2, B - 1):
+        assert abs(float((o[b].double() - ro).mean())) <= bound, b
+
+
 def test_decode_scales_of_very_different_size():
     """Value groups whose scales differ by tokens and groups up to 2^30, the smallest with
     the weight: each output keeps its precision relative to what its own group holds."""
