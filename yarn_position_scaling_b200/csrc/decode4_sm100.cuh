@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     constexpr int kRow = kv4_row_bytes(HD), G = HD / kKv4Group;
     static_assert(REP == 1 || (NT == 1 && REP <= G), "columns to spare");
     // A step takes 16 H keys through scores and outputs.  Two halves overlap; with one query head
-    // a KV head, where the work on p s is least, one at a time spills less (77 against 81 us on
-    // 16 windowed sequences of 32 KV heads, but 175 against 167 on 8 long ones with REP = 2).
+    // a KV head, where the work on p s is least, one at a time spills less (78 against 86 us on
+    // 16 windowed sequences of 32 KV heads, but 183 against 175 on 8 long ones with REP = 2).
     constexpr int H = REP == 4 ? 1 : 2;
     constexpr int GL = G / REP;       // groups of a lane in the value product: k REP + copy
     constexpr int kCopy = 4 / REP;    // lanes r of a copy; the next copy is as far away
@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
 
             // With kShare the outputs of group k REP + copy are in o[k]: the copies' columns take
             // turns, each group's B operand being zero in the others'.  It saves registers (d =
-            // 128: 175 -> 167 us); where there are enough, the zeroing costs more (d = 64: 78 -> 81).
+            // 128: 195 -> 175 us on 8 long sequences of 8 KV heads); where there are enough, the
+            // zeroing costs more (d = 64: 45.8 -> 47.3 us on 4 sequences of 60K keys and 8 heads).
             constexpr bool kShare = REP > 1 && HD == 128;
             constexpr int GO = kShare ? GL : G;
             float o[GO][2][NT][4], w[NT][2][GL], l[NT][2], R[NT][2];

@@ -313,16 +313,18 @@ namespace yr_host {
 // copies (110 ps a row) and then holds 256 query rows a tile, with a window 128, however few
 // there are (95 ps a row and query head, with a window half).  At d = 64 the products of the
 // prefill kernel are half as long but its softmax is not.  Both sides measured, decode and
-// prefill kernel: after 120K keys of 8 KV heads with 32 query heads 4 tokens 77 and 464 us, 16
-// tokens 245 and 465, 32 tokens 469 and 467; with 64 query heads 16 tokens 470 and 809, 32
-// tokens 922 and 809; d = 64, 20K keys of 4 KV heads with 16 query heads 40 tokens 46 and 49,
-// 48 tokens 51 and 49; window 4096, d = 128 16 tokens 31 and 34, 24 tokens 36 and 36, d = 64
-// 40 tokens 25 and 28.
+// prefill kernel in us: after 120K keys of 8 KV heads with 32 query heads 4 tokens 78 and 462,
+// 16 tokens 257 and 466, 28 tokens 441 and 467, 32 tokens 491 and 466; with 64 query heads 24
+// tokens 732 and 811, 28 tokens 856 and 812; with 8 after 60K 48 tokens 109 and 125, 64 tokens
+// 137 and 125; d = 64, 20K keys of 4 KV heads with 16 query heads 40 tokens 47 and 49, 48 tokens
+// 51 and 48; 60K of 16 with 16 48 tokens 119 and 146, 64 tokens 153 and 145; window 4096, 32
+// and 8 heads of d = 128 16 tokens 33 and 34, 20 tokens 36 and 34, 16 and 4 heads of d = 64 40
+// tokens 25 and 28; window 2048, 8 and 8 heads 64 tokens 20 and 24.
 bool chunk4_by_decode(int g, int Tq, int d, int window) {
     if (g > 16) return false;
     const long long tenths = 10ll * decode4_runs(g, Tq).n;
-    if (d == 64) return tenths <= (window > 0 ? 30 + 15 * g : 20 + 22 * g);
-    return tenths <= (window > 0 ? 10 + 10 * g : 17 + 16 * g);
+    if (d == 64) return tenths <= (window > 0 ? 30 + 20 * g : 16 + 22 * g);
+    return tenths <= (window > 0 ? 12 + 8 * g : 15 + 15 * g);
 }
 
 // Bytes that the decode kernel's partial results take for a chunk.
