@@ -498,6 +498,8 @@ int yr_attn_decode_noalloc(const void *q_new, const void *k_new, const void *v_n
  *   k_stored, v_stored bf16 [B, Hkv, d] (nullable): the new row's values as stored
  *   workspace: >= yr_attn_decode_kv4_workspace_bytes(B, Hq, Hkv, d) bytes, 256-byte
  *     aligned, for the partial results.  Calls that overlap need one each.
+ *   If a wait in the kernel runs out of its limit (YR_ETIMEOUT from yr_device_status), the
+ *     heads whose keys were not all read are NaN, in o and lse; the new rows are written.
  *   Precision: the query enters as two fp16 parts (22 bits) scaled by a power of two, the
  *   codes exactly, scales in fp32; probabilities times scales enter the value product as
  *   fp16 relative to the largest; all sums fp32.

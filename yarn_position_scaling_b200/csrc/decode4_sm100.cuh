@@ -48,6 +48,10 @@ struct Decode4Params {
     float sl2;  // softmax scale times log2 e
     int alibi;
     uint64_t timeout_ns;
+    // Failure-detection test hook, compiled only into the test build (YR_FAULT_HOOKS): warp 0 of
+    // one block (-1: none) issues all its copies but one, counted from 0, so a wait that nothing
+    // will complete runs out of time.
+    int fault_block, fault_copy;
     double turns[64];
 };
 
@@ -271,6 +275,9 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     // and the parity of the latter.
     uint32_t s_load = 0, s_wait = 0, parity = 0;
     const uint64_t policy = l2_policy_evict_first();
+#ifdef YR_FAULT_HOOKS
+    int n_copies = 0;
+#endif
 
     // Segments before the first one of this block.
     // 32 at a time, by a sum over the lanes.
@@ -335,6 +342,9 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 ld_key = lo2w;
                 ld_end = hi2;
             }
+            // After a copy that did not land the rest of the share is not read any more; its new rows
+            // are still made.
+            if (sm->abort) ld_key = ld_end;
             int key = ld_key, end = ld_end;
             auto advance = [&](int &k, int &e) {
                 k += kStride;
@@ -344,7 +354,11 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 }
             };
             auto load = [&] {  // the cached rows of the next tile: all but the new one
-                if (lane == 0) {
+                bool issue = lane == 0;
+#ifdef YR_FAULT_HOOKS
+                if (static_cast<int>(blockIdx.x) == p.fault_block && warp == 0 && n_copies++ == p.fault_copy) issue = false;
+#endif
+                if (issue) {
                     const int n = min(kDec4Tile, ld_end - ld_key);
                     const uint32_t bytes = (n - (has_L && ld_key + n > L ? 1 : 0)) * kRow;
                     uint64_t *bar = &sm->full[warp][s_load];
@@ -845,7 +859,6 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                     }
                 }
             __syncthreads();
-            if (sm->abort) return;  // a copy did not land: no partial result to trust
             float *red = reinterpret_cast<float *>(&sm->ring[0][0][0]);  // [warps][8 NT][HD]
 #pragma unroll
             for (int i = 0; i < GO; ++i) {
@@ -878,8 +891,9 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 }
                 p.ws_o[(slot + h) * HD + dim] = acc;
                 if (dim == 0) {
+                    // After a copy that did not land: no earlier call's partial result passes for this one.
                     p.ws_ml[(slot + h) * 2] = top_m;
-                    p.ws_ml[(slot + h) * 2 + 1] = sum;
+                    p.ws_ml[(slot + h) * 2 + 1] = sm->abort ? __int_as_float(0x7fc00000) : sum;
                 }
             }
             fence_proxy_async_smem();  // the ring's next copies follow these writes and reads

@@ -152,6 +152,13 @@ int launch_decode4_call(yr::Decode4Params &dp, int d, const yr_rope_table *tab, 
     dp.alibi = tab->method == YR_ALIBI ? 1 : 0;
     for (int i = 0; i < d / 2; ++i) dp.turns[i] = tab->turns[i];
     dp.timeout_ns = wait_timeout_ns();
+#ifdef YR_FAULT_HOOKS
+    // Test build only: the failure-path hook, read on every launch.
+    const char *drop = std::getenv("YR_FAULT_DROP_KV4_COPY");  // block:copy
+    if (!drop || std::sscanf(drop, "%d:%d", &dp.fault_block, &dp.fault_copy) != 2) dp.fault_block = -1;
+#else
+    dp.fault_block = -1;
+#endif
     const bool half = tab->pairs == YR_PAIR_HALF;
     int rc = d == 128 ? half ? launch_decode4<128, true, kMulti>(dp, sm_count, st)
                          : launch_decode4<128, false, kMulti>(dp, sm_count, st)
