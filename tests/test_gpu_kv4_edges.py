@@ -1,0 +1,125 @@
+"""Edges of the 4-bit KV cache's calls on the GPU: what their documentation allows, far from the
+ordinary sizes and values.  Plain forms in tests/_kv4.py."""
+import math
+
+import pytest
+import torch
+
+from tests import _kv4 as R
+from tests.test_gpu_kv4 import gen_of, new_kv, randn, random_rows, table
+from yarn_position_scaling_b200 import api, build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    api.load()
+
+
+def one_value_rows(z, d):
+    """Cache rows [1, 1, T, 5d/4] whose key's elements are all z[t] (exact in fp16), and whose
+    values are codes of scale 1/8 and minimum -1."""
+    T = z.numel()
+    rows = torch.randint(0, 256, (1, 1, T, 5 * d // 4), dtype=torch.uint8, device="cuda",
+                         generator=gen_of(T))
+    par = torch.zeros(1, 1, T, 2, d // 32, 2, dtype=torch.float16, device="cuda")
+    par[:, :, :, 0, :, 1] = z.half().view(1, 1, T, 1)
+    par[:, :, :, 1, :, 0] = 0.125
+    par[:, :, :, 1, :, 1] = -1.0
+    rows[..., d:] = par.flatten(-3).view(torch.uint8)
+    return rows
+
+
+# ------------------------------------------------------------------- scores of any size
+# Queries of equal elements a over keys of equal elements z: a score is scale a d z.  Keys 2^-9
+# apart are then more than 1000 apart in their scores, so one key has all the weight, and the
+# output is its value as stored: s n + z in one rounding.  The score's error is that of its
+# factors' and sums' roundings, (d + 16) 2^-24 of it at the most.
+HUGE = [1e6, 1e8, 1e10, 1e20, 1e32, 1e35]
+
+
+@pytest.mark.parametrize("a", HUGE + [-x for x in HUGE])
+@pytest.mark.parametrize("Hq,d", [(1, 128), (4, 64), (4, 128), (6, 128), (16, 64), (12, 128)])
+def test_decode_takes_the_largest_of_huge_scores(a, Hq, d):
+    L = 300
+    tab = table(d, method="alibi")  # no rotation, and a bias far below the gaps
+    z = 1 + torch.randperm(L, generator=torch.Generator().manual_seed(L)) / 512
+    rows = torch.cat([one_value_rows(z, d), torch.zeros(1, 1, 1, 5 * d // 4, dtype=torch.uint8, device="cuda")], 2)
+    best = int(z.argmax() if a > 0 else z.argmin())
+    q = torch.full((1, Hq, d), a, device="cuda").bfloat16()
+    k = torch.full((1, 1, d), 0.5 if a > 0 else 3.0, device="cuda").bfloat16()  # never the best
+    lse = torch.empty(1, Hq, device="cuda")
+    o = api.attn_decode_kv4(q, k, k, rows, torch.tensor([L], dtype=torch.int32, device="cuda"), tab, lse=lse)
+    api.device_status()
+    want = R.values(*R.decode_rows(rows[0, :, best])[1]).float().bfloat16()
+    assert torch.equal(o[0], want.expand(Hq, d))
+    score = float(q[0, 0, 0].double()) * d * float(z[best]) * tab.softmax_scale
+    bias = 2.0 ** (-8.0 * torch.arange(1, Hq + 1, device="cuda", dtype=torch.float64) / Hq) * (L - best)
+    assert (lse.double() - (score - bias)).abs().max() <= (d + 17) * 2.0 ** -24 * abs(score)
+
+
+@pytest.mark.parametrize("a", [-1e32, 1e32, -1e9, 3e7])
+@pytest.mark.parametrize("Hq,d", [(1, 128), (4, 64), (4, 128), (8, 128), (16, 128)])
+def test_huge_scores_that_are_equal_share_the_weight(a, Hq, d):
+    """Equal scores stay equal however coarse: the output is the mean of the values.  n codes of
+    scale 1/8 and p = 1 are summed exactly, the division and bf16 round."""
+    L = 700
+    tab = api.rope_freq_table(d, 500000.0, 8192, 16.0, "factors", factors=[1e30] * (d // 2))  # no rotation
+    rows = torch.cat([one_value_rows(torch.ones(L), d), torch.zeros(1, 1, 1, 5 * d // 4, dtype=torch.uint8, device="cuda")], 2)
+    q = torch.full((1, Hq, d), a, device="cuda").bfloat16()
+    score = abs(float(q[0, 0, 0])) * d * tab.softmax_scale
+    k = torch.ones(1, 1, d, device="cuda").bfloat16()
+    lse = torch.empty(1, Hq, device="cuda")
+    o = api.attn_decode_kv4(q, k, k, rows, torch.tensor([L], dtype=torch.int32, device="cuda"), tab, lse=lse)
+    api.device_status()
+    v = R.values(*R.decode_rows(rows[0, 0])[1])
+    want = v.mean(0)
+    assert ((o[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20).all()
+    assert (lse.abs().double() - score).abs().max() <= (d + 17) * 2.0 ** -24 * score
+
+
+@pytest.mark.parametrize("a", [-1e32, 1e32, -1e8])
+def test_a_lone_key_of_a_huge_score_has_the_weight(a):
+    d = 128
+    rows = api.kv4_cache(1, 2, 4, d)
+    gen, tab = gen_of(1), table(d)
+    q = torch.full((1, 8, d), a, device="cuda").bfloat16()
+    k, v = torch.ones(1, 2, d, device="cuda").bfloat16(), randn(gen, 1, 2, d).bfloat16()
+    vs = torch.empty_like(v)
+    o = api.attn_decode_kv4(q, k, v, rows, torch.zeros(1, dtype=torch.int32, device="cuda"), tab, v_stored=vs)
+    api.device_status()
+    assert torch.equal(o.view(2, 4, d), vs.view(2, 1, d).expand(2, 4, d))
+
+
+@pytest.mark.parametrize("a", [1e8, -1e8, 1e32, -1e32])
+@pytest.mark.parametrize("Hq,Tq,d", [(1, 2, 128), (2, 4, 64), (4, 4, 128)])
+def test_short_chunk_takes_the_largest_of_huge_scores(a, Hq, Tq, d):
+    P0 = 300
+    tab = table(d, method="alibi")
+    z = 1 + torch.randperm(P0, generator=torch.Generator().manual_seed(P0)) / 512
+    rows = torch.cat([one_value_rows(z, d), torch.zeros(1, 1, Tq, 5 * d // 4, dtype=torch.uint8, device="cuda")], 2)
+    best = int(z.argmax() if a > 0 else z.argmin())
+    q = torch.full((1, Hq, Tq, d), a, device="cuda").bfloat16()
+    k = torch.full((1, 1, Tq, d), 0.5 if a > 0 else 3.0, device="cuda").bfloat16()
+    o = api.attn_prefill_chunk_kv4(q, k, k, rows, P0, tab)
+    api.device_status()
+    want = R.values(*R.decode_rows(rows[0, :, best])[1]).float().bfloat16()
+    assert torch.equal(o[0], want.expand(Hq, Tq, d))
+
+
+@pytest.mark.parametrize("Hq,d", [(1, 128), (4, 64), (16, 128)])
+def test_a_temperature_that_leaves_no_score_gives_the_mean(Hq, d):
+    """A softmax scale below fp32's range: every score is 0, in the partly filled tile too."""
+    L = 70
+    tab = api.rope_freq_table(d, 500000.0, 8192, 16.0, "factors", factors=[1.0] * (d // 2), attn_factor=1e-30)
+    gen = gen_of(d)
+    rows = torch.cat([one_value_rows(torch.ones(L), d), torch.zeros(1, 1, 1, 5 * d // 4, dtype=torch.uint8, device="cuda")], 2)
+    q, k = randn(gen, 1, Hq, d).bfloat16(), randn(gen, 1, 1, d).bfloat16()
+    lse = torch.empty(1, Hq, device="cuda")
+    o = api.attn_decode_kv4(q, k, k * 0, rows, torch.tensor([L], dtype=torch.int32, device="cuda"), tab, lse=lse)
+    api.device_status()
+    want = R.values(*R.decode_rows(rows[0, 0])[1]).mean(0)
+    assert ((o[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20).all()
+    assert (lse.double() - math.log(L + 1)).abs().max() <= 2.0 ** -20

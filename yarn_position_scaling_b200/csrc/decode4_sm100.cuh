@@ -28,7 +28,10 @@ constexpr int kDec4Stages = 2;
 // output to bf16 gives 0.17%, for 6% of the time (8 sequences 166 -> 175 us; with a fold every 32 or 64
 // tiles the same time and more error, every 8 no less error).
 constexpr int kDec4Fold = 16;
-constexpr float kNoScore = -1e30f;  // the reference of a column that has seen no key yet
+// The reference of a column that has seen no key yet: no finite score lies below it.
+constexpr float kNoScore = -3.402823466e38f;
+// Scores from 2^22 on have units of 0.5 or more, too coarse for a reference a few units off one.
+constexpr float kCoarseScore = 4194304.f;
 
 struct Decode4Params {
     const __nv_bfloat16 *q_new;          // [B][Hq][Tq][d]
@@ -45,7 +48,10 @@ struct Decode4Params {
     int seg_tokens, n_segs;  // tokens of a segment, segments of a sequence and KV head
     int grid_blocks;
     int window, n_sink;
-    float sl2;  // softmax scale times log2 e
+    // Softmax scale times log2 e, as a number that goes into the queries and a power of two.  A
+    // score's product with the latter is exact, and so its distance from another in an FMA: with the
+    // whole scale there, the product's unrounded rest, 2^-25 of a score, stood in every exponent.
+    float sl2_part, sl2_pow2;
     int alibi;
     uint64_t timeout_ns;
     // Failure-detection test hook, compiled only into the test build (YR_FAULT_HOOKS): warp 0 of
@@ -215,7 +221,7 @@ struct Decode4Smem {
     float2 q_cs[kMulti ? 1 : HD / 2];  // and for the queries
     uint4 q_hi[8 * NT][HD / 8], q_lo[8 * NT][HD / 8];  // fragments, see the rotation below
     float q_sum[8 * NT][HD / kKv4Group];  // sums of the scaled query over the groups
-    float q_scale[8 * NT];  // what takes the scaled query back
+    float q_scale[8 * NT];  // power of two that makes a score of the scaled query one in log2 units
     float slope[8 * NT];
     float m[kDec4Warps][8 * NT], l[kDec4Warps][8 * NT];
     uint64_t full[kDec4Warps][kDec4Stages];
@@ -243,6 +249,8 @@ constexpr size_t decode4_smem_bytes() {
 //   p z in fp32.  p = 2^(score - R) for a reference R per head that puts the largest p s of
 //   a tile at 2^8 and is raised only once one passes 2^15: small scales keep their bits
 //   (fp16 holds 2^-14 at full precision), and the common tile costs one vote.
+//   Scores are the queries' products times a power of two, so that score - R is exact but for
+//   one rounding however large the scores are.
 template <int HD, int NT, int REP, bool kHalf, bool kMulti>
 __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
     decode4_split_kernel(const __grid_constant__ Decode4Params p) {
@@ -390,19 +398,20 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 }
             }
             // The new row wants its sines in 64 bits; the queries' 22 bits do with fp32 ones.  Of
-            // one token they are shared by its heads, of several each thread computes its own.
+            // one token they are shared by its heads, of several each thread computes its own.  They
+            // carry the softmax scale's part that is not a power of two.
             auto cos_sin = [&](int pos, int i) {
                 const double tr = static_cast<double>(pos) * p.turns[i];
                 float sn, co;
                 sincospif(2.f * static_cast<float>(tr - rint(tr)), &sn, &co);
-                return make_float2(co, sn);
+                return make_float2(co * p.sl2_part, sn * p.sl2_part);
             };
             if constexpr (!kMulti) {
                 for (int i = tid; i < HD / 2; i += kDec4Threads) {
                     if (has_L) {
                         const double2 t = kv4_cos_sin(L, p.turns[i]);
                         sm->cs[i] = t;
-                        sm->q_cs[i] = make_float2(static_cast<float>(t.x), static_cast<float>(t.y));
+                        sm->q_cs[i] = make_float2(static_cast<float>(t.x) * p.sl2_part, static_cast<float>(t.y) * p.sl2_part);
                     } else {
                         sm->q_cs[i] = cos_sin(L, i);
                     }
@@ -462,11 +471,11 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 sm->q_lo[h][ch] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 if ((ch & 3) == 0) sm->q_sum[h][ch >> 2] = sum;
                 if (ch == 0) {
-                    sm->q_scale[h] = pow2i(e2 - 7);
-                    // ALiBi's slope in units of a score before its scaling by sl2 q_scale.
+                    const float back = pow2i(e2 - 7) * p.sl2_pow2;
+                    sm->q_scale[h] = back;
+                    // ALiBi's slope in units of a score before its scaling by q_scale.
                     sm->slope[h] = p.alibi ? exp2f(-8.0f * static_cast<float>(kvh * g + h - dec4_token<kMulti>(p, h) * g + 1) /
-                                                   static_cast<float>(p.Hq)) * 1.4426950408889634f /
-                                                 (p.sl2 * pow2i(e2 - 7))
+                                                   static_cast<float>(p.Hq)) * 1.4426950408889634f / back
                                            : 0.f;
                 }
             }
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 qz[nt] = r < 2 ? *reinterpret_cast<const uint32_t *>(&hv)
                                : pack_half2(z0 - __low2float(hv), z1 - __high2float(hv));
 #pragma unroll
-                for (int j = 0; j < 2; ++j) x_scale[nt][j] = p.sl2 * sm->q_scale[nt * 8 + 2 * (r % kCopy) + j];
+                for (int j = 0; j < 2; ++j) x_scale[nt][j] = sm->q_scale[nt * 8 + 2 * (r % kCopy) + j];
             }
 
             // With kShare the outputs of group k REP + copy are in o[k]: the copies' columns take
@@ -751,7 +760,8 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                 };
                 if (__any_sync(0xffffffffu, products())) {
                     // Raise the references to these keys' largest p s, put at 2^8 (a scale below
-                    // fp16's smallest counts as that).
+                    // fp16's smallest counts as that), or where scores are coarse their largest p
+                    // at 1, which leaves p s at most at fp16's largest scale, 65504 2 / 15.
                     float ls[H][2];
 #pragma unroll
                     for (int t = 0; t < H; ++t)
@@ -768,8 +778,10 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
                         for (int j = 0; j < 2; ++j) {
                             float t = R[nt][j];
 #pragma unroll
-                            for (int k = 0; k < 2 * H; ++k)
-                                t = fmaxf(t, fmaf(x[k >> 1][nt][2 * (k & 1) + j], x_scale[nt][j], ls[k >> 1][k & 1]));
+                            for (int k = 0; k < 2 * H; ++k) {
+                                const float score = x[k >> 1][nt][2 * (k & 1) + j] * x_scale[nt][j];
+                                t = fmaxf(t, fabsf(score) < kCoarseScore ? score + ls[k >> 1][k & 1] : score);
+                            }
 #pragma unroll
                             for (int off = kCopy; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
                             if (!(fabsf(t) < INFINITY)) t = R[nt][j];

@@ -148,7 +148,13 @@ int launch_decode4(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
 template <bool kMulti>
 int launch_decode4_call(yr::Decode4Params &dp, int d, const yr_rope_table *tab, int sm_count,
                         cudaStream_t st) {
-    dp.sl2 = static_cast<float>(tab->softmax_scale * 1.4426950408889634);
+    // The power of two of the scale, as far as its products with the queries' stay within fp32.
+    const double sl2 = tab->softmax_scale * 1.4426950408889634;
+    int sl2_exp = 0;
+    std::frexp(sl2, &sl2_exp);
+    sl2_exp = sl2_exp > 0 ? 0 : sl2_exp < -50 ? -50 : sl2_exp;
+    dp.sl2_part = static_cast<float>(std::ldexp(sl2, -sl2_exp));
+    dp.sl2_pow2 = static_cast<float>(std::ldexp(1.0, sl2_exp));
     dp.alibi = tab->method == YR_ALIBI ? 1 : 0;
     for (int i = 0; i < d / 2; ++i) dp.turns[i] = tab->turns[i];
     dp.timeout_ns = wait_timeout_ns();
