@@ -456,9 +456,10 @@ int yr_attn_decode_noalloc(const void *q_new, const void *k_new, const void *v_n
  *   Each 32 consecutive elements of the rotated key, and of the value, share an fp16 scale
  *   s and minimum z; an element is a code n in 0 .. 15 that stands for s n + z:
  *     z = fp16(min), s = fp16(max(0, (max - z) / 15)), n = clamp(rint((x - z) / s), 0, 15)
- *   (n = 0 where s = 0), fp32 arithmetic, ties to even.  The key is rotated in fp64 and
- *   rounded once to fp32 before that.  An element moves by at most s / 2 plus the fp16
- *   roundings of z and s (15 / 2048 of a step and 2^-11 |z|).
+ *   (n = 0 where s = 0), fp32 arithmetic, ties to even.  The key is rotated in fp64, by
+ *   position times turns[i] taken exactly, and rounded once to fp32 before that; kv4_write
+ *   and the appending calls agree at every position.  An element moves by at most s / 2 plus
+ *   the fp16 roundings of z and s (15 / 2048 of a step and 2^-11 |z|).
  *   Codes lie in the order in which the attention reads them, from the low nibble up, with
  *   G = d / 32: 8 key codes at word r G + g (r = 0 .. 3) for elements 32g + 8r .. + 7, and 4
  *   value codes at 16-bit unit c G + g (c = 0 .. 7) for elements 32g + 4c .. + 3.

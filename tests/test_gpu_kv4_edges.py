@@ -123,3 +123,60 @@ def test_a_temperature_that_leaves_no_score_gives_the_mean(Hq, d):
     want = R.values(*R.decode_rows(rows[0, 0])[1]).mean(0)
     assert ((o[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20).all()
     assert (lse.double() - math.log(L + 1)).abs().max() <= 2.0 ** -20
+
+
+# ----------------------------------------------------------------------- far positions
+def exact_angles(pos, tab):
+    """(cos, sin) of pos times the table's turns, the product without a rounding: turns split into
+    a 24-bit part, whose product with a position below 2^29 is exact, and the rest."""
+    t = R.turns_of(tab).cuda()
+    hi = t.float().double()
+    n = pos.double().unsqueeze(-1)
+    frac = n * hi
+    frac = (frac - torch.round(frac) + n * (t - hi)) * (2.0 * math.pi)
+    return torch.cos(frac), torch.sin(frac)
+
+
+def turn(x, c, s, pairs):
+    """Pairs of x [..., T, d] in 64 bits turned by the angles of c, s [T, d/2]."""
+    if pairs == "half":
+        u, w = x.chunk(2, -1)
+        return torch.cat([u * c - w * s, u * s + w * c], -1)
+    u, w = x[..., 0::2], x[..., 1::2]
+    return torch.stack([u * c - w * s, u * s + w * c], -1).flatten(-2)
+
+
+@pytest.mark.parametrize("pairs", ["interleaved", "half"])
+@pytest.mark.parametrize("pos0", [(1 << 20) - 17, (1 << 28) - 17, (1 << 28) + 12345])
+def test_far_positions_are_rotated_as_defined(pos0, pairs):
+    """Keys whose rotated elements lie within a few hundredths of a large number: a step of a code
+    is 2^-11 of that number, so an angle that is off by 2^-25, the rounding of position times turns
+    at 2^28, moves one code in some thousands.  The rows are those of the definition, and a decode
+    step writes the same ones."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    d, T = 64, 1000
+    tab = api.rope_freq_table(d, 10000.0, 8192, 1.0, "rope", pairs=pairs)
+    cache = torch.empty(1, 1, pos0 + T, 80, dtype=torch.uint8, device="cuda")
+    gen = gen_of(pos0 % 1000)
+    pos = pos0 + torch.arange(T, device="cuda")
+    c, s = exact_angles(pos, tab)
+    for _ in range(40):
+        y = 1000.0 + randn(gen, 1, 1, T, d)
+        k = turn(y.double(), c, -s, pairs).bfloat16()
+        v = randn(gen, 1, 1, T, d).bfloat16()
+        api.kv4_write(k, v, cache, tab, pos0=pos0)
+        rows = cache[:, :, pos0:]
+        want = R.quantise(turn(k.double(), c, s, pairs).float()), R.quantise(v.float())
+        for got, w in zip(R.decode_rows(rows), want):
+            assert all(torch.equal(a, b) for a, b in zip(got, w))
+    api.device_status()
+    written = cache[:, :, pos0: pos0 + 64].clone()
+    cache[:, :, pos0: pos0 + 64] = 0
+    ws = torch.empty(api.attn_decode_kv4_workspace_bytes(1, 1, 1, d), dtype=torch.uint8, device="cuda")
+    for t in range(64):
+        api.attn_decode_kv4(k[:, :, t].contiguous(), k[:, :, t].contiguous(), v[:, :, t].contiguous(), cache,
+                            torch.tensor([pos0 + t], dtype=torch.int32, device="cuda"), tab, window=1,
+                            workspace=ws)
+    api.device_status()
+    assert torch.equal(cache[:, :, pos0: pos0 + 64], written)

@@ -401,9 +401,9 @@ __global__ void __launch_bounds__(kDec4Threads, NT == 2 ? 2 : 4)
             // one token they are shared by its heads, of several each thread computes its own.  They
             // carry the softmax scale's part that is not a power of two.
             auto cos_sin = [&](int pos, int i) {
-                const double tr = static_cast<double>(pos) * p.turns[i];
+                const double n = static_cast<double>(pos), tr = n * p.turns[i];
                 float sn, co;
-                sincospif(2.f * static_cast<float>(tr - rint(tr)), &sn, &co);
+                sincospif(2.f * static_cast<float>(tr - rint(tr) + fma(n, p.turns[i], -tr)), &sn, &co);
                 return make_float2(co * p.sl2_part, sn * p.sl2_part);
             };
             if constexpr (!kMulti) {

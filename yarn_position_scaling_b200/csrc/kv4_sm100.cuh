@@ -7,9 +7,10 @@
 // stands for s n + z with the group's fp16 scale s and minimum z:
 //   z = fp16(min x),  s = fp16(max(0, (max x - z) / 15)),
 //   n = clamp(rint((x - z) / s), 0, 15), or 0 where s = 0,
-// in fp32 with ties to even; the key is rotated in fp64 and rounded once to fp32, so that
-// a code does not depend on how a sine was approximated.  s n is exact in fp32 (an 11-bit
-// times a 4-bit integer), so s n + z has one rounding.
+// in fp32 with ties to even; the key is rotated in fp64, by the position times the table's turns
+// without a rounding of that product, and rounded once to fp32: the sines' own errors, 2^-49 in
+// the passes here, reach a code only where an fp32 tie and a code's border meet.  s n is exact in
+// fp32 (an 11-bit times a 4-bit integer), so s n + z has one rounding.
 // Code order: a key word (8 codes) at index r G + g holds elements 32g + 8r .. + 7, a value
 // unit (4 codes) at index c G + g holds elements 32g + 4c .. + 3 (G = d/32, r in 0..3,
 // c in 0..7, codes from the low bits up).  The lanes of one matrix fragment of the decode
@@ -104,11 +105,12 @@ __device__ __forceinline__ bool kv4_clamp(float &x) {
     return bad;
 }
 
-// cos and sin of position * 2 pi turns, the angle reduced to one turn first.
+// cos and sin of position * 2 pi turns, the angle reduced to one turn first: exactly, with the
+// product's rounding (up to 2^-26 turns at 2^30, which the reduction would leave in the angle) put back.
 __device__ __forceinline__ double2 kv4_cos_sin(int pos, double turns) {
-    const double tr = __dmul_rn(static_cast<double>(pos), turns);
+    const double n = static_cast<double>(pos), tr = __dmul_rn(n, turns);
     double sn, cs;
-    sincospi(2.0 * __dsub_rn(tr, rint(tr)), &sn, &cs);
+    sincospi(2.0 * __dadd_rn(__dsub_rn(tr, rint(tr)), fma(n, turns, -tr)), &sn, &cs);
     return make_double2(cs, sn);
 }
 
@@ -263,7 +265,8 @@ __device__ __forceinline__ void kv4_quantise_row(const float (&x)[G][8], int r, 
 
 // A block takes 32 rows of one sequence and `heads` KV heads in turn, and computes the sines
 // of its positions once for them: by angle addition from row to row, 16 (8) rows from a start
-// that is computed (16 products cost 2^-49).
+// that is computed (16 products cost 2^-49; the start's angle has no error that grows with its
+// position, or all its rows would have it).
 template <int HD, bool kHalf>
 __global__ void __launch_bounds__(kKv4WriteThreads) kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
     constexpr int G = HD / kKv4Group, kPairs = HD / 2, kRows = kKv4WriteRows;
