@@ -1,6 +1,10 @@
 """Edges of the 4-bit KV cache's calls on the GPU: what their documentation allows, far from the
 ordinary sizes and values.  Plain forms in tests/_kv4.py."""
 import math
+import os
+import subprocess
+import sys
+import textwrap
 
 import pytest
 import torch
@@ -180,3 +184,33 @@ def test_far_positions_are_rotated_as_defined(pos0, pairs):
                             workspace=ws)
     api.device_status()
     assert torch.equal(cache[:, :, pos0: pos0 + 64], written)
+
+
+# ---------------------------------------------------------- first use inside a capture
+CAPTURE_CHILD = textwrap.dedent(f"""
+    import sys
+    sys.path.insert(0, {os.path.dirname(os.path.dirname(os.path.abspath(__file__)))!r})
+    import torch
+    from yarn_position_scaling_b200 import api
+    from tests.test_gpu_kv4 import gen_of, random_rows, randn, table
+    tab, gen, L = table(128), gen_of(1), 100
+    q, k = randn(gen, 1, 16, 128).bfloat16(), randn(gen, 1, 2, 128).bfloat16()
+    kv, cl = random_rows(gen, 1, 2, L + 1, 128), torch.tensor([L], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.empty(api.attn_decode_kv4_workspace_bytes(1, 16, 2, 128), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.attn_decode_kv4(q, k, k, kv, cl, tab, out=out, workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(api.attn_decode_kv4(q, k, k, kv, cl, tab), out)
+    api.device_status()
+    print("CAPTURED")
+""")
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """A kernel form is set up at its first launch, which may be one into a graph."""
+    r = subprocess.run([sys.executable, "-c", CAPTURE_CHILD], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "CAPTURED" in r.stdout, r.stdout + r.stderr

@@ -110,20 +110,36 @@ Decode4Runs decode4_runs(int g, int Tq) {
     return {tokens, (Tq + tokens - 1) / tokens};
 }
 
+// Blocks of a split kernel per SM, set up at its first launch in a context: callers without a
+// 4-bit cache do not wait for its 28 forms to be loaded.
+template <int HD, int NT, int REP, bool kHalf, bool kMulti>
+int prepare_decode4_form(unsigned long long ctx, int *per_sm) {
+    static std::mutex mu;
+    static std::unordered_map<unsigned long long, int> by_ctx;
+    std::lock_guard<std::mutex> lk(mu);
+    auto it = by_ctx.find(ctx);
+    if (it == by_ctx.end()) {
+        const auto kernel = &yr::decode4_split_kernel<HD, NT, REP, kHalf, kMulti>;
+        const size_t smem = yr::decode4_smem_bytes<HD, NT, kMulti>();
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+        if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", e);
+        int n = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, yr::kDec4Threads, smem);
+        if (e != cudaSuccess) return cuda_fail("cudaOccupancyMaxActiveBlocksPerMultiprocessor", e);
+        it = by_ctx.emplace(ctx, n > 0 ? n : 1).first;
+    }
+    *per_sm = it->second;
+    return YR_OK;
+}
+
 // One wave of the split kernel, and the places of its partial results.
 template <int HD, int NT, int REP, bool kHalf, bool kMulti>
-int launch_decode4_form(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
-    static int per_sm = 0;  // same value on every device of this build's target
-    if (per_sm == 0) {
-        int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &n, yr::decode4_split_kernel<HD, NT, REP, kHalf, kMulti>, yr::kDec4Threads,
-                yr::decode4_smem_bytes<HD, NT, kMulti>()) != cudaSuccess ||
-            n < 1)
-            n = 1;
-        per_sm = n;
-    }
-    const int blocks = per_sm * sm_count;
+int launch_decode4_form(yr::Decode4Params &dp, const DeviceState &dev, cudaStream_t st) {
+    int per_sm = 0;
+    const int rc = prepare_decode4_form<HD, NT, REP, kHalf, kMulti>(dev.ctx, &per_sm);
+    if (rc != YR_OK) return rc;
+    const int blocks = per_sm * dev.sm_count;
     dp.grid_blocks = blocks < yr::kDec4MaxBlocks ? blocks : yr::kDec4MaxBlocks;
     const long long slots = dp.grid_blocks + static_cast<long long>(dp.B) * dp.n_segs * dp.Hkv;
     dp.ws_ml = dp.ws_o + slots * dp.seg_tokens * dp.group * HD;
@@ -136,17 +152,17 @@ int launch_decode4_form(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
 
 // The form of the kernel for a segment's columns (tokens times query heads per KV head).
 template <int HD, bool kHalf, bool kMulti>
-int launch_decode4(yr::Decode4Params &dp, int sm_count, cudaStream_t st) {
+int launch_decode4(yr::Decode4Params &dp, const DeviceState &dev, cudaStream_t st) {
     const int cols = dp.seg_tokens * dp.group;
-    if (cols > 8) return launch_decode4_form<HD, 2, 1, kHalf, kMulti>(dp, sm_count, st);
-    if (cols > 4) return launch_decode4_form<HD, 1, 1, kHalf, kMulti>(dp, sm_count, st);
-    if (cols > 2 || HD == 64) return launch_decode4_form<HD, 1, 2, kHalf, kMulti>(dp, sm_count, st);
-    return launch_decode4_form<HD, 1, HD / 32, kHalf, kMulti>(dp, sm_count, st);
+    if (cols > 8) return launch_decode4_form<HD, 2, 1, kHalf, kMulti>(dp, dev, st);
+    if (cols > 4) return launch_decode4_form<HD, 1, 1, kHalf, kMulti>(dp, dev, st);
+    if (cols > 2 || HD == 64) return launch_decode4_form<HD, 1, 2, kHalf, kMulti>(dp, dev, st);
+    return launch_decode4_form<HD, 1, HD / 32, kHalf, kMulti>(dp, dev, st);
 }
 
 // The split kernel over dp's segments and the merge of its partial results.
 template <bool kMulti>
-int launch_decode4_call(yr::Decode4Params &dp, int d, const yr_rope_table *tab, int sm_count,
+int launch_decode4_call(yr::Decode4Params &dp, int d, const yr_rope_table *tab, const DeviceState &dev,
                         cudaStream_t st) {
     // The power of two of the scale, as far as its products with the queries' stay within fp32.
     const double sl2 = tab->softmax_scale * 1.4426950408889634;
@@ -166,10 +182,10 @@ int launch_decode4_call(yr::Decode4Params &dp, int d, const yr_rope_table *tab, 
     dp.fault_block = -1;
 #endif
     const bool half = tab->pairs == YR_PAIR_HALF;
-    int rc = d == 128 ? half ? launch_decode4<128, true, kMulti>(dp, sm_count, st)
-                         : launch_decode4<128, false, kMulti>(dp, sm_count, st)
-         : half   ? launch_decode4<64, true, kMulti>(dp, sm_count, st)
-                  : launch_decode4<64, false, kMulti>(dp, sm_count, st);
+    int rc = d == 128 ? half ? launch_decode4<128, true, kMulti>(dp, dev, st)
+                         : launch_decode4<128, false, kMulti>(dp, dev, st)
+         : half   ? launch_decode4<64, true, kMulti>(dp, dev, st)
+                  : launch_decode4<64, false, kMulti>(dp, dev, st);
     if (rc != YR_OK) return rc;
     // The merge may start, and find its pieces, while the split kernel still runs; it waits
     // for that kernel's results itself.
@@ -295,8 +311,8 @@ extern "C" int yr_attn_decode_kv4(const void *q_new, const void *k_new, const vo
             return fail(YR_EINVAL, f + ": tensor pointers must be 16-byte aligned");
     if (!aligned(cache_len, 4) || (lse && !aligned(lse, 4)))
         return fail(YR_EINVAL, f + ": cache_len and lse must be 4-byte aligned");
-    int sm_count = 0;
-    rc = prepare_device(&sm_count);
+    DeviceState dev;
+    rc = prepare_device(nullptr, &dev);
     if (rc != YR_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int g = Hq / Hkv;
@@ -315,7 +331,7 @@ extern "C" int yr_attn_decode_kv4(const void *q_new, const void *k_new, const vo
     dp.window = window; dp.n_sink = n_sink;
     dp.Tq = 1; dp.seg_tokens = 1; dp.n_segs = 1;
     dp.ws_o = static_cast<float *>(workspace);
-    return launch_decode4_call<false>(dp, d, tab, sm_count, st);
+    return launch_decode4_call<false>(dp, d, tab, dev, st);
 }
 
 namespace yr_host {
@@ -384,9 +400,10 @@ extern "C" int yr_attn_prefill_chunk_kv4(const void *q, const void *k_new, const
     if (rc != YR_OK) return rc;
     for (const void *ptr : {k_new, v_new})
         if (!aligned(ptr, 16)) return fail(YR_EINVAL, f + ": pointers must be 16-byte aligned");
-    int sm_count = 0;
-    rc = prepare_device(&sm_count);
+    DeviceState dev;
+    rc = prepare_device(nullptr, &dev);
     if (rc != YR_OK) return rc;
+    const int sm_count = dev.sm_count;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     long long ks[3];
     strides_or_contiguous(nullptr, Hkv, Tq, d, ks);
@@ -407,7 +424,7 @@ extern "C" int yr_attn_prefill_chunk_kv4(const void *q, const void *k_new, const
         dp.P0 = P0; dp.Tq = Tq; dp.seg_tokens = runs.tokens; dp.n_segs = runs.n;
         dp.window = window; dp.n_sink = n_sink;
         dp.ws_o = static_cast<float *>(workspace);
-        return launch_decode4_call<true>(dp, d, tab, sm_count, st);
+        return launch_decode4_call<true>(dp, d, tab, dev, st);
     }
     // The rows in 16 bits for the attention: with a window, the 128-key tiles that it reads
     // and no others (those of the sinks, and from the first query's window on).

@@ -115,6 +115,7 @@ struct DeviceState {
     bool sm100 = false;
     bool prefill_regs_ok = false;  // launched register count covers the setmaxnreg split
     int sm_count = 0;
+    unsigned long long ctx = 0;
 };
 std::mutex g_dev_mu;
 std::unordered_map<unsigned long long, DeviceState> g_dev;  // by context id
@@ -133,6 +134,7 @@ int prepare_device(int *sm_count, DeviceState *out = nullptr) {
         if (e != cudaSuccess) return cuda_fail("cudaGetDeviceProperties", e);
         st.sm100 = (prop.major == 10 && prop.minor == 0);
         st.sm_count = prop.multiProcessorCount;
+        st.ctx = ctx;
         if (st.sm100) {
             struct {
                 const void *fn;
@@ -154,19 +156,6 @@ int prepare_device(int *sm_count, DeviceState *out = nullptr) {
                  yr::decode_smem_bytes<64>()},
                 {reinterpret_cast<const void *>(&yr::decode_split_kernel<64, 2>),
                  yr::decode_smem_bytes<64>()},
-#define YR_DECODE4(HD, NT, REP, kHalf)                                                        \
-    {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, kHalf, false>),    \
-     yr::decode4_smem_bytes<HD, NT, false>()},                                                \
-        {reinterpret_cast<const void *>(&yr::decode4_split_kernel<HD, NT, REP, kHalf, true>), \
-         yr::decode4_smem_bytes<HD, NT, true>()}
-                YR_DECODE4(128, 1, 4, false), YR_DECODE4(128, 1, 4, true),
-                YR_DECODE4(128, 1, 2, false), YR_DECODE4(128, 1, 2, true),
-                YR_DECODE4(128, 1, 1, false), YR_DECODE4(128, 1, 1, true),
-                YR_DECODE4(128, 2, 1, false), YR_DECODE4(128, 2, 1, true),
-                YR_DECODE4(64, 1, 2, false), YR_DECODE4(64, 1, 2, true),
-                YR_DECODE4(64, 1, 1, false), YR_DECODE4(64, 1, 1, true),
-                YR_DECODE4(64, 2, 1, false), YR_DECODE4(64, 2, 1, true),
-#undef YR_DECODE4
             };
             for (auto &a : attrs) {
                 e = cudaFuncSetAttribute(a.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
