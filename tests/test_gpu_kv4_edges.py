@@ -214,3 +214,36 @@ def test_first_call_of_a_process_may_be_captured():
     """A kernel form is set up at its first launch, which may be one into a graph."""
     r = subprocess.run([sys.executable, "-c", CAPTURE_CHILD], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "CAPTURED" in r.stdout, r.stdout + r.stderr
+
+
+# ------------------------------------------------------------------- two threads at once
+def test_two_threads_call_at_once():
+    """First calls of a form from two threads, each on a stream of its own: the one-time set-up is
+    shared, the results are those of calls in turn."""
+    import threading
+    cases = []
+    for i, Hq in enumerate((8, 24)):
+        gen, L = gen_of(70 + i), 2000
+        q = randn(gen, 1, Hq, 64).bfloat16()
+        k, v = (x.squeeze(2) for x in new_kv(gen, 1, 2, 1, 64))
+        cases.append((q, k, v, random_rows(gen, 1, 2, L + 1, 64), torch.tensor([L], dtype=torch.int32, device="cuda")))
+    kc = torch.randn(1, 2, 100, 64, device="cuda").bfloat16()
+    tab, got = table(64, "half"), [None, None]
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            start.wait()
+            for _ in range(20):
+                got[i] = api.attn_decode_kv4(*cases[i], tab)
+                api.attn_decode(*cases[i][:3], kc.clone(), kc.clone(), torch.tensor([50], dtype=torch.int32, device="cuda"), tab)
+            torch.cuda.current_stream().synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    api.device_status()
+    for c, g in zip(cases, got):
+        assert torch.equal(api.attn_decode_kv4(*c, tab), g)

@@ -239,16 +239,15 @@ size_t decode_ws_bytes(long long B, long long Hq, long long Hkv, long long d, in
 // equal shares of the balanced split all run at once.
 template <int HD, int NT>
 int decode_grid(int sm_count) {
-    static int per_sm = 0;  // same value on every device of this build's target
-    if (per_sm == 0) {
+    static const int per_sm = [] {  // same value on every device of this build's target
         int n = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, yr::decode_split_kernel<HD, NT>,
                                                           yr::kDecThreads,
                                                           yr::decode_smem_bytes<HD>()) != cudaSuccess ||
             n < 1)
             n = 1;
-        per_sm = n;
-    }
+        return n;
+    }();
     return per_sm * sm_count;
 }
 
