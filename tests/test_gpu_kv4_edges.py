@@ -247,3 +247,40 @@ def test_two_threads_call_at_once():
     api.device_status()
     for c, g in zip(cases, got):
         assert torch.equal(api.attn_decode_kv4(*c, tab), g)
+
+
+# ----------------------------------------------------- the largest windows and sinks
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("window,n_sink", [(BIG, 0), (BIG, BIG), (BIG - 100, 3), (1, BIG), (64, BIG - 60)])
+@pytest.mark.parametrize("Tq", [1, 5, 200])
+def test_largest_windows_and_sinks_over_the_4_bit_cache(window, n_sink, Tq):
+    """They hide nothing: windows of the whole length, bit for bit."""
+    gen, tab, P0, d = gen_of(Tq), table(128), 700, 128
+    rows = random_rows(gen, 1, 2, P0 + Tq, d)
+    q = randn(gen, 1, 8, Tq, d).bfloat16()
+    k, v = new_kv(gen, 1, 2, Tq, d)
+    lse = [torch.empty(1, 8, Tq, device="cuda") for _ in range(2)]
+    plain = (window, P0 + Tq) if window < BIG - 100 else (P0 + Tq, 0)
+    want = api.attn_prefill_chunk_kv4(q, k, v, rows, P0, tab, *plain, lse=lse[0])
+    got = api.attn_prefill_chunk_kv4(q, k, v, rows, P0, tab, window, n_sink, lse=lse[1])
+    assert torch.equal(got, want) and torch.equal(*lse)
+    if Tq == 1:
+        one = [x.squeeze(2).contiguous() for x in (q, k, v)]
+        cl = torch.tensor([P0], dtype=torch.int32, device="cuda")
+        want = api.attn_decode_kv4(*one, rows, cl, tab, *plain)
+        assert torch.equal(api.attn_decode_kv4(*one, rows, cl, tab, window, n_sink), want)
+    api.device_status()
+
+
+@pytest.mark.parametrize("window,n_sink", [(BIG, 0), (BIG, BIG), (BIG - 100, 3), (1, BIG)])
+def test_largest_windows_and_sinks_of_a_prefill(window, n_sink):
+    gen, tab, T, d = gen_of(5), table(64), 300, 64
+    q = randn(gen, 1, 4, T, d).bfloat16()
+    k, v = new_kv(gen, 1, 2, T, d)
+    plain = (window, T) if window == 1 else (T, 0)
+    want = api.attn_prefill(q, k, v, tab, window=plain[0], n_sink=plain[1])
+    got = api.attn_prefill(q, k, v, tab, window=window, n_sink=n_sink)
+    api.device_status()
+    assert torch.equal(got, want)

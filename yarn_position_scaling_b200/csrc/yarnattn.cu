@@ -439,7 +439,11 @@ int launch_attend(const void *q, void *o, float *lse, float *q_rot_dbg, int B, i
     pp.q_dbg = q_rot_dbg;
     pp.B = B; pp.Hq = Hq; pp.Hkv = Hkv; pp.T = T; pp.group = Hq / Hkv;
     pp.Tk = Tk; pp.q_off = q_off; pp.k_pos0 = k_pos0;
-    pp.causal = causal; pp.window = window; pp.n_sink = n_sink;
+    pp.causal = causal;
+    // No distance reaches q_off + T and no key Tk: larger windows and sinks mean the same, and
+    // those near 2^31 would pass it in the kernel's sums.
+    pp.window = window > 0 && window > q_off + T ? q_off + T : window;
+    pp.n_sink = n_sink < Tk ? n_sink : Tk;
     // Windowed calls with an even number of query heads per KV head: a CTA takes two heads of
     // one group at the same 128 rows, so both query tiles see the same key tiles.
     pp.head_pair = attend_head_pair(Hq, Hkv, window);
