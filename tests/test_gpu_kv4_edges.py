@@ -284,3 +284,137 @@ def test_largest_windows_and_sinks_of_a_prefill(window, n_sink):
     got = api.attn_prefill(q, k, v, tab, window=window, n_sink=n_sink)
     api.device_status()
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------- workspaces, tiny caches, graphs
+def guarded(n, fill):
+    """A workspace of n bytes of `fill`, and the bytes behind it, which must stay as they are."""
+    whole = torch.full((n + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    whole[:n] = fill
+    return whole[:n], whole[n:]
+
+
+@pytest.mark.parametrize("lens", [[0], [0, 0, 0], [1, 300, 0, 5000], [127] * 40, [3] * 300, [20000, 1]])
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 2, 128), (8, 2, 128), (16, 2, 64), (32, 2, 128)])
+def test_decode_reads_only_what_it_wrote_into_its_workspace(lens, Hq, Hkv, d):
+    gen, tab, B, T_max = gen_of(len(lens)), table(d), len(lens), max(lens) + 1
+    rows = random_rows(gen, B, Hkv, T_max, d)
+    q = randn(gen, B, Hq, d).bfloat16()
+    k, v = (x.squeeze(2) for x in new_kv(gen, B, Hkv, 1, d))
+    cl, outs = torch.tensor(lens, dtype=torch.int32, device="cuda"), []
+    for fill in (0, 255):
+        ws, behind = guarded(api.attn_decode_kv4_workspace_bytes(B, Hq, Hkv, d), fill)
+        lse = torch.empty(B, Hq, device="cuda")
+        outs.append((api.attn_decode_kv4(q, k, v, rows, cl, tab, workspace=ws, lse=lse), lse))
+        assert (behind == 0xAB).all()
+    api.device_status()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert torch.isfinite(outs[0][0].float()).all() and torch.isfinite(outs[0][1]).all()
+
+
+@pytest.mark.parametrize("P0,Tq,window,n_sink", [(0, 1, 0, 0), (0, 5, 0, 0), (3000, 7, 0, 0), (3000, 7, 100, 5),
+                                                 (700, 130, 0, 0), (3000, 130, 500, 200)])
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(1, 2, 2, 128), (3, 8, 2, 64), (1, 16, 1, 128)])
+def test_chunk_reads_only_what_it_wrote_into_its_workspace(B, Hq, Hkv, d, P0, Tq, window, n_sink):
+    gen, tab = gen_of(P0 + Tq), table(d)
+    rows = random_rows(gen, B, Hkv, P0 + Tq, d)
+    q = randn(gen, B, Hq, Tq, d).bfloat16()
+    k, v = new_kv(gen, B, Hkv, Tq, d)
+    outs = []
+    for fill in (0, 255):
+        ws, behind = guarded(api.attn_prefill_chunk_kv4_workspace_bytes(B, Hq, Hkv, Tq, d, P0), fill)
+        lse = torch.empty(B, Hq, Tq, device="cuda")
+        outs.append((api.attn_prefill_chunk_kv4(q, k, v, rows, P0, tab, window, n_sink, workspace=ws, lse=lse), lse))
+        assert (behind == 0xAB).all()
+    api.device_status()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert torch.isfinite(outs[0][0].float()).all() and torch.isfinite(outs[0][1]).all()
+
+
+def test_decode_of_very_many_sequences():
+    """More sequences than a grid axis holds: zero queries, so the LSE counts each one's keys."""
+    B, d = 70000, 64
+    rows = torch.zeros(B, 1, 9, 80, dtype=torch.uint8, device="cuda")
+    lens = torch.arange(B, device="cuda", dtype=torch.int32) % 9
+    q, tab = torch.zeros(B, 1, d, dtype=torch.bfloat16, device="cuda"), table(d)
+    v = (torch.arange(B, device="cuda") % 128 + 1.0).bfloat16().view(B, 1, 1).expand(B, 1, d).contiguous()
+    lse = torch.empty(B, 1, device="cuda")
+    o = api.attn_decode_kv4(q, v, v, rows, lens, tab, lse=lse)
+    api.device_status()
+    n = (lens + 1).double().view(B, 1)
+    # Scales of 0 put the reference at -32 and log2 of the sum between 32 and 64, where its unit is
+    # 2^-18; their sum is exact, and ln 2 of it rounds once.
+    assert (lse.double() - n.log()).abs().max() <= 2.0 ** -18 * math.log(2.0) + 2.0 ** -22
+    want = v.double() / n.unsqueeze(-1)  # the new row alone is not 0, and is its minimum, exactly
+    assert ((o.double() - want).abs() <= 2.0 ** -8 * want).all()
+
+
+@pytest.mark.parametrize("Tq", [3, 150])
+def test_captured_write_chunk_and_read(Tq):
+    """One graph of a ragged write, a chunk by either kernel and a read, replayed with new inputs."""
+    gen, tab, d, Hq, Hkv, P0, T = gen_of(Tq), table(128), 128, 8, 2, 400, 60
+    q = randn(gen, 1, Hq, Tq, d).bfloat16()
+    k, v = new_kv(gen, 1, Hkv, Tq, d)
+    kp, vp = new_kv(gen, 1, Hkv, T, d)
+    starts = torch.tensor([7], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([50], dtype=torch.int32, device="cuda")
+    first = random_rows(gen, 1, Hkv, P0 + Tq, d)
+    ws = torch.empty(api.attn_prefill_chunk_kv4_workspace_bytes(1, Hq, Hkv, Tq, d, P0), dtype=torch.uint8, device="cuda")
+
+    def run(rows, o, kr, vr):
+        api.kv4_write(kp, vp, rows, tab, starts=starts, counts=counts)
+        api.attn_prefill_chunk_kv4(q, k, v, rows, P0, tab, out=o, workspace=ws)
+        api.kv4_read(rows, T, starts=starts, counts=counts, k=kr, v=vr)
+
+    def outs():
+        return torch.zeros_like(q), torch.zeros_like(kp), torch.zeros_like(vp)
+    rows, captured = first.clone(), outs()
+    run(rows, *captured)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(rows, *captured)
+    for step in range(3):
+        for x in (q, k, v, kp, vp):
+            x.copy_(torch.randn_like(x))
+        starts.fill_(11 * step)
+        counts.fill_(60 - 30 * step)
+        rows.copy_(first)
+        for x in captured:
+            x.zero_()
+        graph.replay()
+        other, plain = first.clone(), outs()
+        run(other, *plain)
+        assert torch.equal(rows, other) and all(torch.equal(a, b) for a, b in zip(captured, plain))
+    api.device_status()
+
+
+# --------------------------------------------------- values outside the range, appended
+@pytest.mark.parametrize("bad", [65536.0, -1e30, math.inf, math.nan])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("Tq", [0, 3, 150])
+def test_appended_values_outside_the_range_are_reported_and_stored_finite(bad, which, Tq):
+    """By a decode step (Tq = 0) and by chunks of either kernel; other heads' rows are as without."""
+    gen, tab, d, P0, n = gen_of(Tq), table(64), 64, 90, max(Tq, 1)
+    rows = random_rows(gen, 1, 2, P0 + n, d)
+    q = randn(gen, 1, 4, n, d).bfloat16()
+    kv = dict(zip("kv", new_kv(gen, 1, 2, n, d)))
+
+    def call(rows):
+        if Tq == 0:
+            one = [x.squeeze(2).contiguous() for x in (q, kv["k"], kv["v"])]
+            return api.attn_decode_kv4(*one, rows, torch.tensor([P0], dtype=torch.int32, device="cuda"), tab)
+        return api.attn_prefill_chunk_kv4(q, kv["k"], kv["v"], rows, P0, tab)
+    plain = rows.clone()
+    want = call(plain)
+    api.device_status()
+    kv[which][0, 1, n - 1, 40] = bad
+    got = call(rows)
+    with pytest.raises(api.YarnAttnError) as ei:
+        api.device_status()
+    assert ei.value.code == api.YR_ERANGE
+    assert torch.equal(rows[:, 0], plain[:, 0]) and torch.equal(rows[:, 1, : P0 + n - 1], plain[:, 1, : P0 + n - 1])
+    for x in api.kv4_read(rows, P0 + n):
+        assert torch.isfinite(x.float()).all()
+    api.device_status()
+    assert torch.equal(got.view(2, -1)[0], want.view(2, -1)[0])
