@@ -54,10 +54,11 @@ struct Decode4Params {
     float sl2_part, sl2_pow2;
     int alibi;
     uint64_t timeout_ns;
-    // Failure-detection test hook, compiled only into the test build (YR_FAULT_HOOKS): warp 0 of
-    // one block (-1: none) issues all its copies but one, counted from 0, so a wait that nothing
-    // will complete runs out of time.
+#ifdef YR_FAULT_HOOKS
+    // Failure-detection test hook, in the test build only: warp 0 of one block (-1: none) issues
+    // all its copies but one, counted from 0, so a wait that nothing will complete runs out of time.
     int fault_block, fault_copy;
+#endif
     double turns[64];
 };
 

@@ -111,25 +111,25 @@ Decode4Runs decode4_runs(int g, int Tq) {
 }
 
 // Blocks of a split kernel per SM, set up at its first launch in a context: callers without a
-// 4-bit cache do not wait for its 28 forms to be loaded.
+// 4-bit cache do not wait for its 28 forms to be loaded.  (Two threads may both set it up.)
 template <int HD, int NT, int REP, bool kHalf, bool kMulti>
-int prepare_decode4_form(unsigned long long ctx, int *per_sm) {
-    static std::mutex mu;
-    static std::unordered_map<unsigned long long, int> by_ctx;
-    std::lock_guard<std::mutex> lk(mu);
-    auto it = by_ctx.find(ctx);
-    if (it == by_ctx.end()) {
+int prepare_decode4_form(const DeviceState &dev, int *per_sm) {
+    constexpr int form = (HD == 128 ? 16 : 0) + (NT == 2 ? 12 : REP == 1 ? 8 : REP == 2 ? 4 : 0) +
+                         (kHalf ? 2 : 0) + (kMulti ? 1 : 0);
+    static_assert(form < kDecode4Forms, "forms");
+    int n = dev.decode4_per_sm[form].load(std::memory_order_acquire);
+    if (n == 0) {
         const auto kernel = &yr::decode4_split_kernel<HD, NT, REP, kHalf, kMulti>;
         const size_t smem = yr::decode4_smem_bytes<HD, NT, kMulti>();
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
         if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", e);
-        int n = 0;
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, yr::kDec4Threads, smem);
         if (e != cudaSuccess) return cuda_fail("cudaOccupancyMaxActiveBlocksPerMultiprocessor", e);
-        it = by_ctx.emplace(ctx, n > 0 ? n : 1).first;
+        n = n > 0 ? n : 1;
+        dev.decode4_per_sm[form].store(n, std::memory_order_release);
     }
-    *per_sm = it->second;
+    *per_sm = n;
     return YR_OK;
 }
 
@@ -137,7 +137,7 @@ int prepare_decode4_form(unsigned long long ctx, int *per_sm) {
 template <int HD, int NT, int REP, bool kHalf, bool kMulti>
 int launch_decode4_form(yr::Decode4Params &dp, const DeviceState &dev, cudaStream_t st) {
     int per_sm = 0;
-    const int rc = prepare_decode4_form<HD, NT, REP, kHalf, kMulti>(dev.ctx, &per_sm);
+    const int rc = prepare_decode4_form<HD, NT, REP, kHalf, kMulti>(dev, &per_sm);
     if (rc != YR_OK) return rc;
     const int blocks = per_sm * dev.sm_count;
     dp.grid_blocks = blocks < yr::kDec4MaxBlocks ? blocks : yr::kDec4MaxBlocks;
@@ -178,8 +178,6 @@ int launch_decode4_call(yr::Decode4Params &dp, int d, const yr_rope_table *tab, 
     // Test build only: the failure-path hook, read on every launch.
     const char *drop = std::getenv("YR_FAULT_DROP_KV4_COPY");  // block:copy
     if (!drop || std::sscanf(drop, "%d:%d", &dp.fault_block, &dp.fault_copy) != 2) dp.fault_block = -1;
-#else
-    dp.fault_block = -1;
 #endif
     const bool half = tab->pairs == YR_PAIR_HALF;
     int rc = d == 128 ? half ? launch_decode4<128, true, kMulti>(dp, dev, st)

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -110,12 +111,14 @@ int current_context(int *dev_out, unsigned long long *ctx_id) {
     return YR_OK;
 }
 
+constexpr int kDecode4Forms = 32;
+
 // Per-context one-time set-up: architecture check and shared-memory opt-in.
 struct DeviceState {
     bool sm100 = false;
     bool prefill_regs_ok = false;  // launched register count covers the setmaxnreg split
     int sm_count = 0;
-    unsigned long long ctx = 0;
+    std::atomic<int> *decode4_per_sm = nullptr;  // of the 4-bit decode's forms, 0: not set up yet
 };
 std::mutex g_dev_mu;
 std::unordered_map<unsigned long long, DeviceState> g_dev;  // by context id
@@ -134,7 +137,7 @@ int prepare_device(int *sm_count, DeviceState *out = nullptr) {
         if (e != cudaSuccess) return cuda_fail("cudaGetDeviceProperties", e);
         st.sm100 = (prop.major == 10 && prop.minor == 0);
         st.sm_count = prop.multiProcessorCount;
-        st.ctx = ctx;
+        st.decode4_per_sm = new std::atomic<int>[kDecode4Forms]();
         if (st.sm100) {
             struct {
                 const void *fn;
