@@ -506,9 +506,12 @@ int yr_attn_decode_noalloc(const void *q_new, const void *k_new, const void *v_n
  *   fp16 relative to the largest; all sums fp32.
  *
  * attn_prefill_chunk_kv4 -- yr_attn_prefill_chunk over this cache: writes the chunk's rows
- *   into slots P0 .. P0+Tq-1 and attends over the rows 0 .. P0+Tq-1.  A few tokens (up to
- *   about 30) are taken by the decode kernel, with its precision, over the 4-bit rows; more
- *   by the prefill kernel, over fp16 copies of the rows that the call makes in the workspace.
+ *   into slots P0 .. P0+Tq-1 and attends over the rows 0 .. P0+Tq-1.  A few tokens are taken
+ *   by the decode kernel, with its precision, over the 4-bit rows; more by the prefill kernel,
+ *   over fp16 copies of the rows that the call makes in the workspace.  The border depends on
+ *   d, Hq/Hkv and whether there is a window: at d = 128 15 to 48 tokens without one (28 at
+ *   Hq/Hkv = 4) and 8 to 32 with one (16), at d = 64 21 to 80 (40 and 44), fewer with more
+ *   heads; with Hq/Hkv > 16 it is always the prefill kernel.
  *   A chunk's own keys are attended as stored, so the result does not depend on where a
  *   prompt is cut (up to rounding), and Tq = 1 is a decode step.  With a window only the
  *   rows that some query of the chunk sees are used.

@@ -540,8 +540,8 @@ def _kv4_call(dev, fn, args, stream):
 
 
 def kv4_write(k, v, kv4, table: RopeTable, pos0: int = 0, starts=None, counts=None, stream=None):
-    """Rotate, quantise and write k, v [B,Hkv,T,d] bf16 (any strides with unit stride over d)
-    into the 4-bit cache: row t of sequence b goes to slot pos0 + starts[b] + t.  starts and
+    """Rotate, quantise and write k, v [B,Hkv,T,d] bf16 (unit stride over d, the others positive
+    multiples of 8) into the 4-bit cache: row t of sequence b goes to slot pos0 + starts[b] + t.  starts and
     counts are int32 [B] on the device (None: 0 and T); rows t >= counts[b] are left out.
     Returns kv4."""
     B, Hkv, T, d = k.shape
@@ -561,8 +561,8 @@ def kv4_read(kv4, T: int, pos0: int = 0, starts=None, counts=None, dtype=torch.b
     """Rows of the 4-bit cache as values: row t of sequence b from slot pos0 + starts[b] + t,
     t < counts[b] (starts, counts as in kv4_write).  Returns (k, v) [B,Hkv,T,d] in `dtype`
     (bf16 or fp16), zero in the rows that are not read.  Outputs given as k and v are written
-    in place (any strides with unit stride over d) and keep those rows; if one is given, the
-    other is not read and comes back as None."""
+    in place (strides as in kv4_write) and keep those rows; if one is given, the other is not
+    read and comes back as None."""
     fn = "kv4_read"
     if dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("kv4_read: dtype must be torch.bfloat16 or torch.float16")

@@ -22,11 +22,11 @@ constexpr int kDec4Threads = kDec4Warps * 32;
 constexpr int kDec4Tile = 32;  // keys of one bulk copy
 constexpr int kDec4Stages = 2;
 // The tensor cores' fp32 sums are cut off, not rounded, and the sum of p s n, all positive, is far
-// larger than the output where values of both signs cancel: over 128K keys of like weight a warp's
-// 28K keys (48 sequences, 8 KV heads) gave 1.7% error, its 4.4K keys (8 sequences) 0.25%.  So the
-// accumulators are folded into rounded sums every 16 tiles: 0.19% and 0.18%, where rounding the
-// output to bf16 gives 0.17%, for 6% of the time (8 sequences 166 -> 175 us; with a fold every 32 or 64
-// tiles the same time and more error, every 8 no less error).
+// larger than the output where values of both signs cancel: over 128K keys of like weight, 8 KV
+// heads, a warp's 21K keys (48 sequences) give 1.2 - 1.3% error and its 3.5K keys (8 sequences)
+// 0.24%.  So the accumulators are folded into rounded sums every 16 tiles: 0.17 - 0.18% for both,
+// where rounding the output to bf16 gives 0.16 - 0.17%, for up to 2% of the time (8 sequences 287.6
+// -> 289.5 us; with a fold every 32 or 64 tiles 0.18 and 0.19 - 0.20%, every 8 no less error).
 constexpr int kDec4Fold = 16;
 // The reference of a column that has seen no key yet: no finite score lies below it.
 constexpr float kNoScore = -3.402823466e38f;

@@ -346,7 +346,10 @@ namespace yr_host {
 // 137 and 125; d = 64, 20K keys of 4 KV heads with 16 query heads 40 tokens 47 and 49, 48 tokens
 // 51 and 48; 60K of 16 with 16 48 tokens 119 and 146, 64 tokens 153 and 145; window 4096, 32
 // and 8 heads of d = 128 16 tokens 33 and 34, 20 tokens 36 and 34, 16 and 4 heads of d = 64 40
-// tokens 25 and 28; window 2048, 8 and 8 heads 64 tokens 20 and 24.
+// tokens 25 and 28; window 2048, 8 and 8 heads 64 tokens 20 and 24.  The window's length does not
+// move the border: 32 and 8 heads, 32K 16 tokens 86 and 105, 24 tokens 120 and 106, 64K 16 tokens
+// 147 and 178, 20 tokens 183 and 178, 128K (all of 120K) 20 tokens 318 and 310, 24 tokens 378 and
+// 313, by the prefill kernel's 128-row form, which calls without a window do not take.
 bool chunk4_by_decode(int g, int Tq, int d, int window) {
     if (g > 16) return false;
     const long long tenths = 10ll * decode4_runs(g, Tq).n;
