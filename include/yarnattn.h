@@ -169,7 +169,9 @@ size_t yr_attn_prefill_workspace_bytes(int B, int Hkv, int T, int d);
  *   |rotated q|, |rotated k| and |v| must stay below 65520, the fp16 range: a
  *   value outside it (or a NaN) sets the range bit of the device status word,
  *   which yr_device_status() then reports as YR_ERANGE; the output of such a
- *   call is unspecified.  The probabilities are kept within fp16 by the kernel.
+ *   call is unspecified.  The probabilities are kept within fp16 by the kernel, for
+ *   scaled logits up to 10^8 in magnitude: 2^-25 of a logit, the rounding of its product
+ *   with the scale, stands in the exponent of a row's probabilities and of its LSE.
  * Errors: YR_EINVAL (shapes, strides, alignment, flags, workspace too small),
  *   YR_EUNSUPPORTED (d not 64 or 128, device not sm_100), YR_ECUDA.
  */
@@ -516,7 +518,8 @@ int yr_attn_decode_noalloc(const void *q_new, const void *k_new, const void *v_n
  *   prompt is cut (up to rounding), and Tq = 1 is a decode step.  With a window only the
  *   rows that some query of the chunk sees are used.
  *   q, o bf16 [B, Hq, Tq, d]; k_new, v_new bf16 [B, Hkv, Tq, d], contiguous; lse fp32
- *   [B, Hq, Tq] (nullable); q must stay in the fp16 range as in yr_attn_prefill.
+ *   [B, Hq, Tq] (nullable); q and the scaled logits must stay in the ranges of
+ *   yr_attn_prefill (the decode kernel takes any).
  *   workspace: 256-byte aligned; yr_attn_prefill_chunk_kv4_workspace_bytes() gives room
  *     for the fp16 rows and for the split-KV partials of either kernel.  The former are
  *     needed -- yr_attn_prefill_workspace_bytes(B, Hkv, P0 + Tq, d) rounded up to 256 --
